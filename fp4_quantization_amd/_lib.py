@@ -25,6 +25,9 @@ RECIPE_UFP4, RECIPE_UFP4_INT4, RECIPE_NVFP4 = 0, 1, 2
 GEMM_FWD_Y, GEMM_BWD_DX, GEMM_BWD_DW = 0, 1, 2
 OPERAND_A, OPERAND_B = 0, 1
 TENSOR_X, TENSOR_W, TENSOR_DY = 0, 1, 2
+TYPE_BF16, TYPE_F32 = 0, 1
+CKPT_INT8, CKPT_E4M3 = 0, 1
+ACT_SILU, ACT_GELU_TANH = 0, 1
 
 EXPORTED = ["ufp4_status_string", "ufp4_workspace_size", "ufp4_workspace_init",
             "ufp4_workspace_status", "ufp4_quantize", "ufp4_quantize_rowcol",
@@ -32,7 +35,10 @@ EXPORTED = ["ufp4_status_string", "ufp4_workspace_size", "ufp4_workspace_init",
             "ufp4_rht_signs", "ufp4_grouped_col_offsets", "ufp4_time_rowcol", "ufp4_set_schedule",
             "ufp4_schedule_of", "ufp4_amax_tiles", "ufp4_quantize_delayed", "ufp4_gemm_nt",
             "ufp4_recipe_config", "ufp4_f32_to_bf16", "ufp4_quantize_rowcol_noalloc",
-            "ufp4_quantize_grouped_delayed", "ufp4_roof_rowcol"]
+            "ufp4_quantize_grouped_delayed", "ufp4_roof_rowcol",
+            "ufp4_expert_rows", "ufp4_expert_sort", "ufp4_expert_dispatch", "ufp4_expert_dispatch_checkpoint",
+            "ufp4_expert_combine", "ufp4_expert_combine_backward", "ufp4_checkpoint_save", "ufp4_checkpoint_load",
+            "ufp4_gated_act", "ufp4_gated_act_backward", "ufp4_gemm_grouped_nt", "ufp4_gemm_grouped_dw"]
 
 
 class Ufp4Error(RuntimeError):
@@ -121,6 +127,23 @@ def _load():
     L.ufp4_recipe_config.argtypes = [i32, i32, i32, u64, u64, cfgp, ctypes.POINTER(i32), ctypes.POINTER(i32)]
     L.ufp4_schedule_of.restype = ctypes.c_int
     L.ufp4_schedule_of.argtypes = [i64, i64, i32, i32, cfgp, ctypes.POINTER(i32)]
+    L.ufp4_expert_rows.restype = i64
+    L.ufp4_expert_rows.argtypes = [i64, i32, i32, i32]
+    for name, args in (
+            ("ufp4_expert_sort", [P, i64, i32, i64, i32, i32, i64, P, P, P, P]),
+            ("ufp4_expert_dispatch", [P, i64, i64, i64, i32, P, P, i64, P, i64, P]),
+            ("ufp4_expert_dispatch_checkpoint", [P, P, i32, i64, i64, i32, P, P, i64, P, i64, P]),
+            ("ufp4_expert_combine", [P, i32, i64, i64, i64, P, P, i64, i32, P, i32, i64, P]),
+            ("ufp4_expert_combine_backward",
+             [P, i32, i64, i64, i64, i32, P, i32, i64, i64, P, P, P, P, i64, P, P]),
+            ("ufp4_checkpoint_save", [P, i64, i64, i64, i32, P, P, P]),
+            ("ufp4_checkpoint_load", [P, P, i64, i64, i32, P, i32, i64, P]),
+            ("ufp4_gated_act", [P, i64, i64, i64, i32, P, i64, i32, P, P, P]),
+            ("ufp4_gated_act_backward", [P, i64, P, P, i32, i64, i64, i32, P, i64, P, i64, P]),
+            ("ufp4_gemm_grouped_nt", [cfgp, i64, i64, i64, ufp4_qtensor, ufp4_qtensor, i32, P, i32, P, i32, i64, P]),
+            ("ufp4_gemm_grouped_dw", [cfgp, i64, i64, i64, ufp4_qtensor, ufp4_qtensor, P, i32, P, i32, P])):
+        getattr(L, name).restype = ctypes.c_int
+        getattr(L, name).argtypes = args
     return L
 
 

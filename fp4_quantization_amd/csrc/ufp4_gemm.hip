@@ -27,78 +27,13 @@
 // the block scale.
 #include <hip/hip_runtime.h>
 
+#include "ufp4_expand.hpp"
 #include "ufp4_internal.hpp"
 
 namespace ufp4 {
 
-typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef uint32_t g32x2 __attribute__((ext_vector_type(2)));
-typedef uint32_t g32x4 __attribute__((ext_vector_type(4)));
-
 constexpr int kGemmM = 256, kGemmN = 256, kGemmK = 64;
 constexpr int kGemmLd = kGemmK + 8;  // fp16 per LDS row: 144 bytes, 16-byte aligned rows
-
-// High bytes of the fp16 encodings of the grid magnitudes by magnitude
-// index (low word: indices 0..3, high word: 4..7).
-template <int GRID>
-__device__ __forceinline__ uint32_t f16_hi_lo() {
-  return GRID == kGridINT4 ? 0x42403C00u : 0x3E3C3800u;  // {0, 1, 2, 3} / {0, .5, 1, 1.5}
-}
-template <int GRID>
-__device__ __forceinline__ uint32_t f16_hi_hi() {
-  return GRID == kGridE1M2 ? 0x43424140u    // 2, 2.5, 3, 3.5
-         : GRID == kGridINT4 ? 0x47464544u  // 4, 5, 6, 7
-                             : 0x46444240u; // 2, 3, 4, 6 (E2M1; the clamped grid uses 0..4)
-}
-
-// Two's-complement nibbles -> sign-magnitude nibbles, eight at a time (for
-// a negative nibble n, |n| = (n ^ 7) + 1 with the sign bit kept).
-__device__ __forceinline__ uint32_t signmag8(uint32_t P) {
-  const uint32_t A = P & 0x88888888u, S = A >> 3;
-  return (P ^ (A - S)) + S;
-}
-
-// Eight codes (element 2i in the low nibble of byte i) to four fp16 pairs
-// times the block scale d2 = (d, d).
-template <int GRID>
-__device__ __forceinline__ void expand8(uint32_t word, f16x2 d2, uint32_t out[4]) {
-  if (GRID == kGridINT4) word = signmag8(word);
-  const uint32_t lo = f16_hi_lo<GRID>(), hi = f16_hi_hi<GRID>();
-  // high bytes of the even (low-nibble) and odd (high-nibble) elements; the
-  // sign bits are merged by one three-input bitwise op, a | (b & c)
-  // (truth table 0xF8)
-  const uint32_t he = (uint32_t)__builtin_amdgcn_bitop3_b32(__builtin_amdgcn_perm(hi, lo, word & 0x07070707u),
-                                                             word << 4, 0x80808080u, 0xF8);
-  const uint32_t ho = (uint32_t)__builtin_amdgcn_bitop3_b32(__builtin_amdgcn_perm(hi, lo, (word >> 4) & 0x07070707u),
-                                                             word, 0x80808080u, 0xF8);
-  // (element 2i, element 2i+1) = (0x00, he.byte i, 0x00, ho.byte i); selector
-  // 0x0C gives a zero byte, 0..3 the bytes of he, 4..7 those of ho
-  out[0] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x040C000Cu)) * d2);
-  out[1] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x050C010Cu)) * d2);
-  out[2] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x060C020Cu)) * d2);
-  out[3] = __builtin_bit_cast(uint32_t, __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x070C030Cu)) * d2);
-}
-
-// One 16-element block: 8 code bytes and its E4M3 scale byte, to 16 fp16
-// values (eight words, element 2i in the low half of word i).
-template <int GRID>
-__device__ __forceinline__ void expand16(g32x2 codes, uint32_t sbyte, uint32_t o[8]) {
-  // the hardware OCP E4M3 decode of the (non-negative) scale byte; exact,
-  // and every E4M3 value is an fp16 value
-  const _Float16 d = (_Float16)__builtin_amdgcn_cvt_pk_f32_fp8((int)(sbyte & 0x7Fu), false)[0];
-  const f16x2 d2 = {d, d};
-  expand8<GRID>(codes.x, d2, o);
-  expand8<GRID>(codes.y, d2, o + 4);
-}
-
-// The 16 fp16 values of a block to dst (16-byte aligned).
-__device__ __forceinline__ void store16(const uint32_t o[8], _Float16* dst) {
-  g32x4* p = reinterpret_cast<g32x4*>(dst);
-  p[0] = g32x4{o[0], o[1], o[2], o[3]};
-  p[1] = g32x4{o[4], o[5], o[6], o[7]};
-}
 
 // Grid: (ceil(N/256), ceil(M/256)); 512 threads (8 waves).  Wave w computes
 // the 64 x 128 sub-tile at rows 64 (w / 2), columns 128 (w % 2), as 2 x 4

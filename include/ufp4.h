@@ -334,6 +334,148 @@ int ufp4_quantize_grouped_delayed(const uint16_t* x, int64_t total_rows, int64_t
                                   ufp4_qtensor row_out, ufp4_qtensor col_out, void* ws, size_t ws_bytes,
                                   ufp4_stream_t stream);
 
+/* --- expert layer: rows to experts and back -------------------------------- */
+
+/* The token side of the grouped (MoE) calls: T tokens with `slots` chosen
+ * experts each.  Slot s = t * slots + j holds token t's j-th expert id;
+ * an id outside [0, num_experts) is a dropped slot (it has no row).
+ * Element types of the calls below that take one: */
+enum ufp4_type { UFP4_BF16 = 0, UFP4_F32 = 1 };
+
+/* Rows that ufp4_expert_sort needs for any routing of tokens * slots slots
+ * when every segment is padded to a multiple of `align`: tokens * slots +
+ * min(num_experts, tokens * slots) * (align - 1), rounded up to a multiple of
+ * align; 0 for invalid arguments.  Host only. */
+int64_t ufp4_expert_rows(int64_t tokens, int32_t slots, int32_t num_experts, int32_t align);
+
+/* Stable sort of the slots by expert, the row order of the grouped calls.
+ *   ids: int32 [tokens][ld_ids >= slots] on the device.
+ *   offsets: int64 [num_experts + 2].  Segment e < num_experts is rows
+ *     [offsets[e], offsets[e+1]): first the slots of expert e in slot order,
+ *     then padding up to a multiple of align rows.  Segment num_experts is the
+ *     rest, up to offsets[num_experts + 1] = total_rows, so the grouped
+ *     quantizer takes the array as it is, with num_experts + 1 segments and
+ *     (for align a multiple of its block) padded_rows = total_rows, and no
+ *     count has to come back to the host.
+ *   row_of_slot: int32 [tokens][slots], the row of each slot, -1 if dropped.
+ *   slot_of_row: int32 [total_rows], the slot of each row, -1 for padding.
+ *   total_rows >= ufp4_expert_rows(...); total_rows and tokens * slots below
+ *     2^28, here and in the calls below (UFP4_ERR_SHAPE).
+ * 1 <= num_experts <= 1023, 1 <= slots <= 1024, 1 <= align <= 4096
+ * (UFP4_ERR_INVALID_ARGUMENT).  The outputs must not overlap ids. */
+int ufp4_expert_sort(const int32_t* ids, int64_t tokens, int32_t slots, int64_t ld_ids, int32_t num_experts,
+                     int32_t align, int64_t total_rows, int64_t* offsets, int32_t* row_of_slot,
+                     int32_t* slot_of_row, ufp4_stream_t stream);
+
+/* out[r] = x[slot_of_row[r] / slots] (bf16 rows of `cols` values, leading
+ * dimensions ld and ldo >= cols), zeros for padding rows.  row_of_slot and
+ * slot_of_row as ufp4_expert_sort writes them; an entry of row_of_slot outside
+ * [0, total_rows) counts as dropped.  Any cols >= 0 and any 2-byte alignment;
+ * the gradient of this call is ufp4_expert_combine without weights. */
+int ufp4_expert_dispatch(const uint16_t* x, int64_t tokens, int64_t cols, int64_t ld, int32_t slots,
+                         const int32_t* row_of_slot, const int32_t* slot_of_row, int64_t total_rows, uint16_t* out,
+                         int64_t ldo, ufp4_stream_t stream);
+
+/* out[t] = sum over j of weights[t][j] * z[row_of_slot[t][j]], in slot order,
+ * in fp32, rounded once to out_type; a dropped slot adds nothing whatever its
+ * weight, and a token without slots gets zeros.  z [total_rows][ldz] of z_type,
+ * weights fp32 [tokens][slots] or NULL (all 1), out [tokens][ldo]. */
+int ufp4_expert_combine(const void* z, int32_t z_type, int64_t total_rows, int64_t cols, int64_t ldz,
+                        const int32_t* row_of_slot, const float* weights, int64_t tokens, int32_t slots, void* out,
+                        int32_t out_type, int64_t ldo, ufp4_stream_t stream);
+
+/* Gradients of ufp4_expert_combine for dout [tokens][ldd] of d_type:
+ *   dz[r] = weights[s] * dout[s / slots] with s = slot_of_row[r] (z_type,
+ *     leading dimension lddz, one rounding), zeros for padding rows; every row
+ *     of dz is written.
+ *   dweights[t][j] = sum over columns of dout[t] * z[row_of_slot[t][j]] in
+ *     fp32 in a fixed order, 0 for a dropped slot.
+ * Either output may be NULL (dz NULL leaves slot_of_row unused, dweights NULL
+ * leaves z unused); weights NULL means all 1. */
+int ufp4_expert_combine_backward(const void* dout, int32_t d_type, int64_t tokens, int64_t cols, int64_t ldd,
+                                 int32_t slots, const void* z, int32_t z_type, int64_t total_rows, int64_t ldz,
+                                 const int32_t* row_of_slot, const int32_t* slot_of_row, const float* weights,
+                                 void* dz, int64_t lddz, float* dweights, ufp4_stream_t stream);
+
+/* --- 8-bit activation checkpoints ------------------------------------------ */
+
+/* A rows x cols bf16 matrix kept for the backward pass in 8 bits a value and
+ * one bf16 scale a block of 32 along each row (the last block of a row may be
+ * short): codes [rows][cols], scales [rows][ceil(cols / 32)], both dense.
+ *   Q = 127 (INT8: two's complement) or 448 (E4M3: OCP FP8).
+ *   scale = the smallest bf16 >= amax / Q, at least 2^-100.
+ *   code = value / scale rounded to nearest even; value kept = code * scale,
+ *     exact in fp32.
+ * A block that holds an infinity or a NaN gets the scale NaN (codes 0), so
+ * all of it reads back as NaN. */
+enum ufp4_ckpt_format { UFP4_CKPT_INT8 = 0, UFP4_CKPT_E4M3 = 1 };
+
+int ufp4_checkpoint_save(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld, int32_t format, uint8_t* codes,
+                         uint16_t* scales, ufp4_stream_t stream);
+
+/* out [rows][ldo] = the kept values, as out_type (bf16: one rounding). */
+int ufp4_checkpoint_load(const uint8_t* codes, const uint16_t* scales, int64_t rows, int64_t cols, int32_t format,
+                         void* out, int32_t out_type, int64_t ldo, ufp4_stream_t stream);
+
+/* ufp4_expert_dispatch of a kept matrix of `tokens` rows: what the backward
+ * pass quantizes for the weight gradient, so that a layer keeps its input
+ * once in 8 bits instead of once for every slot. */
+int ufp4_expert_dispatch_checkpoint(const uint8_t* codes, const uint16_t* scales, int32_t format, int64_t tokens,
+                                    int64_t cols, int32_t slots, const int32_t* row_of_slot,
+                                    const int32_t* slot_of_row, int64_t total_rows, uint16_t* out, int64_t ldo,
+                                    ufp4_stream_t stream);
+
+/* Gated activation h = f(g) * u of gu [rows][ld >= 2 width] (bf16; g the first
+ * `width` columns, u the next), in fp32, rounded once to bf16 h [rows][ldh].
+ *   SILU: f(g) = g sigmoid(g).  GELU_TANH: f(g) = g sigmoid(2 sqrt(2/pi)
+ *   (g + 0.044715 g^3)) = g/2 (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))).
+ * With codes not NULL the same pass keeps g and u for the backward pass: codes
+ * [rows][2 width], scales [rows][2 ceil(width / 32)], g's blocks first, then
+ * u's (each as ufp4_checkpoint_save would keep that half). */
+enum ufp4_act { UFP4_ACT_SILU = 0, UFP4_ACT_GELU_TANH = 1 };
+
+int ufp4_gated_act(const uint16_t* gu, int64_t rows, int64_t width, int64_t ld, int32_t act, uint16_t* h, int64_t ldh,
+                   int32_t format, uint8_t* codes, uint16_t* scales, ufp4_stream_t stream);
+
+/* Gradient of the gated activation at the kept values: dgu [rows][lddg >= 2
+ * width] = (dh u f'(g), dh f(g)) for dh [rows][lddh] (bf16, fp32 arithmetic,
+ * one rounding); h_out [rows][ldho], if not NULL, gets f(g) u again, the
+ * weight gradient's operand. */
+int ufp4_gated_act_backward(const uint16_t* dh, int64_t lddh, const uint8_t* codes, const uint16_t* scales,
+                            int32_t format, int64_t rows, int64_t width, int32_t act, uint16_t* dgu, int64_t lddg,
+                            uint16_t* h_out, int64_t ldho, ufp4_stream_t stream);
+
+/* --- expert layer: grouped products ------------------------------------------ */
+
+/* Products of the rows of each segment with that segment's own matrix, all in
+ * one launch, from the quantizer's outputs (NV16; MX32 gives
+ * UFP4_ERR_INVALID_ARGUMENT): for r in [offsets[e], offsets[e+1])
+ *   c[r][n] = sum over k of xa[r][k] * xb_e[n][k],  n < N
+ * a: row-wise layout, codes [total_rows][K/2].  b holds num_groups matrices of
+ * N lines of K: b_layout 0, row-wise (codes [num_groups * N][K/2]: the forward
+ * product, from ufp4_quantize_grouped of the stacked weights with N rows a
+ * segment), or b_layout 1, column-wise (codes [N][num_groups * K/2], segment e
+ * at columns e K: the input gradient's).  a.tensor_scale and b.tensor_scale:
+ * num_groups floats.  offsets_dev: num_groups + 1 int64 (more may follow),
+ * 1 <= num_groups <= 1024, offsets[0] counts as 0; rows behind the last
+ * segment get zeros, and offsets are clamped to [0, total_rows].  c of c_type, leading dimension ldc >= N.
+ * Sums in fp32 of exact products, rounded once.  K % 32 == 0, K and total_rows
+ * below 2^25, N at most 65535 * 256 (UFP4_ERR_SHAPE); codes 16-byte aligned,
+ * block scales 2-byte aligned. */
+int ufp4_gemm_grouped_nt(const ufp4_config* cfg, int64_t total_rows, int64_t N, int64_t K, ufp4_qtensor a,
+                         ufp4_qtensor b, int32_t b_layout, const int64_t* offsets_dev, int32_t num_groups, void* c,
+                         int32_t c_type, int64_t ldc, ufp4_stream_t stream);
+
+/* Weight gradients of every segment: c[e][m][n] = sum over segment e's
+ * (padded) rows of xa[m][r] * xb[n][r], from two column-wise grouped layouts
+ * (codes [M][padded_rows/2] and [N][padded_rows/2], segment e at the columns
+ * ufp4_grouped_col_offsets gives for offsets and a block of 16).  c
+ * [num_groups][M][N] of c_type, dense; an empty segment's matrix is zeros.
+ * padded_rows a multiple of 16 (UFP4_ERR_SHAPE); other rules as above. */
+int ufp4_gemm_grouped_dw(const ufp4_config* cfg, int64_t M, int64_t N, int64_t padded_rows, ufp4_qtensor a,
+                         ufp4_qtensor b, const int64_t* offsets_dev, int32_t num_groups, void* c, int32_t c_type,
+                         ufp4_stream_t stream);
+
 /* --- schedule ------------------------------------------------------------ */
 
 /* Dense NV16 calls need the tensor maximum before any code is written.
