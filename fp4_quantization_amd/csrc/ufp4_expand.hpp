@@ -75,4 +75,43 @@ __device__ __forceinline__ void store16(const uint32_t o[8], _Float16* dst) {
   p[1] = g32x4{o[4], o[5], o[6], o[7]};
 }
 
+// ------------------------------------------------------------------------
+// The grouped products' expansion: the same values times 2^-kExpandShift, in
+// fewer operations.  A sign-magnitude code needs no table if its magnitude m
+// becomes the top bits of an fp16 fraction under the exponents 0 and 1, where
+// fp16 is linear (m 2^-16 for m = 0..7); the sign goes to the sign bit, so two
+// bitwise operations make four high bytes.  The scale is applied as d 2^7 (at
+// most 57344).  For E1M2 the result is value d 2^-8, for INT4 value d 2^-9: a
+// multiple of 2^-18 of at most 11 bits, exact in fp16 (subnormals included,
+// which the MFMA takes as they are).  E2M1 codes have a hardware conversion.
+template <int GRID>
+constexpr int kExpandShift = GRID == kGridE1M2 ? 8 : GRID == kGridINT4 ? 9 : 0;
+
+// The scales of two neighbouring blocks from their E4M3 bytes.
+template <int GRID>
+__device__ __forceinline__ f16x2 expand_scales(uint32_t two_bytes) {
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)(two_bytes & 0x7F7Fu), kExpandShift<GRID> ? 128.0f : 1.0f, false);
+}
+
+template <int GRID>
+__device__ __forceinline__ void expand8_shifted(uint32_t w, f16x2 d, uint32_t out[4]) {
+  f16x2 v[4];
+  if (GRID == kGridE2M1 || GRID == kGridE2M1C) {
+    v[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
+    v[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
+    v[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
+    v[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
+  } else {
+    if (GRID == kGridINT4) w = signmag8(w);
+    const uint32_t he = (w & 0x07070707u) | ((w << 4) & 0x80808080u);
+    const uint32_t ho = ((w >> 4) & 0x07070707u) | (w & 0x80808080u);
+    v[0] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x040C000Cu));
+    v[1] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x050C010Cu));
+    v[2] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x060C020Cu));
+    v[3] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x070C030Cu));
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) out[i] = __builtin_bit_cast(uint32_t, v[i] * d);
+}
+
 }  // namespace ufp4

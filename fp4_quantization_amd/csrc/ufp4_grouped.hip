@@ -13,14 +13,28 @@ namespace ufp4 {
 
 namespace {
 
+// The tile kernel: one workgroup of 12 waves per CU walks over 256 x 256 tiles
+// of C in steps of 64 along the reduction axis.  Four producer waves (one per
+// SIMD) load codes and expand them to fp16 in LDS; eight consumer waves (two
+// per SIMD, each 64 x 128 of the tile) multiply what the producers wrote one
+// step earlier, so the expansion's vector work runs beside the matrix work of
+// other waves instead of between it.  All waves meet in one barrier per step.
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
-constexpr int kTileLd = kTileK + 8;
-constexpr int kTileThreads = 512;
+constexpr int kConsumers = 8, kProducers = 4;
+constexpr int kTileThreads = 64 * (kConsumers + kProducers);
+constexpr int kPieces = (kTileM + kTileN) / (16 * kProducers);  // per producer lane
 
-struct Segment {
-  int32_t e;        // group, `groups` for the rows behind the last one, -1: none
-  int64_t lo, hi;   // rows (nt) or positions along the reduction axis (dw)
-};
+// LDS: [A, B][buffer][line][64 fp16] (both buffers of an operand inside the
+// 16-bit offset of an LDS instruction).  The eight 16-byte chunks of a line are stored in the order chunk ^ swizzle(line):
+// the same chunk of neighbouring lines (a fragment load) and neighbouring
+// chunks of a line (an expansion store) then fall on different banks.
+constexpr int kLineHalves = kTileK;
+__device__ __forceinline__ int swizzle(int line) { return (line >> 1) & 7; }
+__device__ __forceinline__ int lds_at(int line, int chunk) { return line * kLineHalves + 8 * (chunk ^ swizzle(line)); }
+
+// A value that all lanes of the wave hold, as a scalar: branches, loop counts
+// and barriers that depend on it are the wave's.
+__device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 __device__ __forceinline__ int64_t clamp_row(int64_t r, int64_t total) { return r < 0 ? 0 : (r > total ? total : r); }
 
@@ -32,199 +46,305 @@ __device__ __forceinline__ void segment_rows(const GroupedParams& p, int e, int6
   if (e > p.groups || *hi < *lo) *hi = *lo;
 }
 
-// The row tile `tile` of the segments' tiles of `rows` rows, in segment order:
-// its segment and rows.  One wave.
-__device__ __forceinline__ Segment find_tile(const GroupedParams& p, int64_t tile, int rows) {
+// The segments as every workgroup keeps them in LDS.
+//   nt: lo / hi, the rows of segment e (e = groups: the rest), and first, the
+//       number of row tiles before it;
+//   dw: lo / hi, its positions along the column-wise layouts (whole blocks of
+//       16, after those of the segments before it).
+constexpr int kMaxSegments = 1025;
+struct Segments {
+  int32_t lo[kMaxSegments], hi[kMaxSegments], first[kMaxSegments];
+};
+
+// Filled by one wave: 64 segments at a time, their sizes summed over lanes.
+template <bool DW>
+__device__ void fill_segments(const GroupedParams& p, int rows, Segments& S) {
   const int lane = threadIdx.x & 63;
-  Segment r{-1, 0, 0};
+  const int n = DW ? p.groups : p.groups + 1;
   int64_t before = 0;
-  for (int e0 = 0; e0 <= p.groups; e0 += 64) {
+  for (int e0 = 0; e0 < n; e0 += 64) {
+    const int e = e0 + lane;
     int64_t lo, hi;
-    segment_rows(p, e0 + lane <= p.groups ? e0 + lane : p.groups, &lo, &hi);
-    if (e0 + lane > p.groups) hi = lo;
-    const int n = (int)((hi - lo + rows - 1) / rows);
-    int inc = n;
+    segment_rows(p, e < n ? e : p.groups, &lo, &hi);
+    if (e >= n) hi = lo;
+    const int size = DW ? (int)((hi - lo + 15) / 16 * 16) : (int)((hi - lo + rows - 1) / rows);
+    int inc = size;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int o = __shfl_up(inc, d);
       if (lane >= d) inc += o;
     }
-    const int64_t first = before + inc - n;
-    const uint64_t hit = __ballot(tile >= first && tile < first + n);
+    if (e < n) {
+      const int64_t first = before + inc - size;
+      S.lo[e] = (int32_t)(DW ? clamp_row(first, p.total_rows) : lo);
+      S.hi[e] = (int32_t)(DW ? clamp_row(first + size, p.total_rows) : hi);
+      if (!DW) S.first[e] = (int32_t)first;
+    }
+    before += uniform(__shfl(inc, 63));
+  }
+}
+
+// Rows [lo, hi) of the row tile `tile` (of `rows` rows) and its segment, -1 if
+// there are fewer tiles.  One wave.
+struct RowTile {
+  int32_t e, lo, hi;
+};
+__device__ __forceinline__ RowTile find_tile(const GroupedParams& p, const Segments& S, int tile, int rows) {
+  const int lane = threadIdx.x & 63;
+  for (int e0 = 0; e0 <= p.groups; e0 += 64) {
+    const int e = e0 + lane < p.groups ? e0 + lane : p.groups;
+    const int lo = S.lo[e], hi = S.hi[e], at = lo + (tile - S.first[e]) * rows;
+    const uint64_t hit = __ballot(tile >= S.first[e] && at < hi);
     if (hit) {
       const int src = __ffsll((unsigned long long)hit) - 1;
-      r.e = e0 + src;
-      r.lo = __shfl(lo, src) + (tile - __shfl(first, src)) * rows;
-      const int64_t end = __shfl(hi, src);
-      r.hi = r.lo + rows < end ? r.lo + rows : end;
-      return r;
+      const int from = uniform(__shfl(at, src)), end = uniform(__shfl(hi, src));
+      return RowTile{uniform(__shfl(e, src)), from, from + rows < end ? from + rows : end};
     }
-    before += __shfl(inc, 63);
   }
-  return r;
+  return RowTile{-1, 0, 0};
 }
 
-// Positions of segment e along the column-wise layouts: whole blocks of 16,
-// after those of the segments before it.  One wave.
-__device__ __forceinline__ Segment find_columns(const GroupedParams& p, int e) {
-  const int lane = threadIdx.x & 63;
-  int64_t before = 0, mine = 0;
-  for (int e0 = 0; e0 <= e; e0 += 64) {
-    const int i = e0 + lane;
-    int64_t n = 0;
-    if (i <= e) {
-      const int64_t lo = i == 0 ? 0 : clamp_row(p.offsets[i], p.total_rows);
-      const int64_t hi = clamp_row(p.offsets[i + 1], p.total_rows);
-      n = hi > lo ? (hi - lo + 15) / 16 * 16 : 0;
-    }
-    if (i < e) before += n;
-    if (i == e) mine = n;
-  }
-#pragma unroll
-  for (int d = 32; d >= 1; d >>= 1) {
-    before += __shfl_xor(before, d);
-    mine += __shfl_xor(mine, d);
-  }
-  return Segment{e, clamp_row(before, p.total_rows), clamp_row(before + mine, p.total_rows)};
+// Two neighbouring values of a row of C, n of them inside it.
+__device__ __forceinline__ void store_c(float* c, float v0, float v1, int n) {
+  if (n >= 2)
+    store_8<4>(c, v32x2{__float_as_uint(v0), __float_as_uint(v1)});
+  else if (n == 1)
+    *c = v0;
+}
+struct __attribute__((packed, aligned(2))) Pair16 {
+  uint32_t w;
+};
+__device__ __forceinline__ void store_c(uint16_t* c, float v0, float v1, int n) {
+  if (n >= 2)
+    reinterpret_cast<Pair16*>(c)->w = pack_bf16(v0, v1);
+  else if (n == 1)
+    *c = to_bf16(v0);
 }
 
-__device__ __forceinline__ void store_c(float* c, float v) { __builtin_nontemporal_store(v, c); }
-__device__ __forceinline__ void store_c(uint16_t* c, float v) { *c = to_bf16(v); }
+// The line of B (of each 64) that LDS row r holds: columns 2 i and 2 i + 1 of
+// C come from the same lane of two neighbouring column tiles of 32, so a lane
+// stores them together and a row of a store is 64 neighbouring columns.
+__device__ __forceinline__ int b_line_of(int r) { return 2 * (r & 31) + (r >> 5); }
 
-// nt: grid (row tiles, column tiles); dw: grid (column tiles, row tiles,
-// groups).  Eight waves, each 64 x 128 of the 256 x 256 tile.
+// One tile's place: rows [m0, m_end) of A and C, lines n0.. of B, the
+// reduction range of K values at ka / kb, matrix e.  e < 0: no such tile.
+struct Tile {
+  int32_t e;
+  bool live;  // false: rows behind the last segment, zeros
+  int32_t m0, m_end, n0, K, ka;
+  int64_t kb, b_line;
+};
+// Tile ids: column tiles innermost, then row tiles, then (dw) groups.
+struct TileGrid {
+  uint32_t tiles;
+  FastDiv nt, mt;
+};
+template <bool DW>
+__device__ __forceinline__ Tile tile_at(const GroupedParams& p, const Segments& S, uint32_t id, const TileGrid& g) {
+  const uint32_t row = g.nt.div(id);
+  const int32_t n0 = (int32_t)(id - row * g.nt.d) * kTileN;
+  if (DW) {
+    const uint32_t e = g.mt.div(row);
+    const int lo = uniform(S.lo[e]), hi = uniform(S.hi[e]);
+    return Tile{(int32_t)e, true, (int32_t)(row - e * g.mt.d) * kTileM, (int32_t)p.M, n0, hi - lo, lo, lo, 0};
+  }
+  const RowTile s = find_tile(p, S, (int)row, kTileM);
+  const int e = uniform(s.e);
+  const bool live = e < p.groups;
+  return Tile{e, live, uniform(s.lo), uniform(s.hi), n0, live ? (int32_t)p.K : 0, 0, live ? e * p.b.seg_k : 0,
+              live ? e * p.b.seg_lines : 0};
+}
+
+// One operand's lines of a tile as bounds-checked buffers: loads of lines past
+// the last one give zeros.  A line has fewer than 2^24 bytes of codes, so the
+// 256 lines of a tile stay inside 32-bit offsets.
+struct Lines {
+  __amdgpu_buffer_rsrc_t codes, scales;
+};
+__device__ __forceinline__ Lines lines_of(const GroupedOperand& o, int64_t line, int64_t count, int64_t k) {
+  const int64_t n = count < kTileM ? count : kTileM, at = line * o.pitch + k, len = n * o.pitch - k;
+  const uint32_t bytes = (uint32_t)(len / 2);
+  // word 3: 32-bit data, raw addressing
+  return Lines{__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.codes + at / 2), 0, (int)bytes, 0x00020000),
+               __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(o.scales + at / 16), 0, (int)(bytes / 8), 0x00020000)};
+}
+
+// 32 values of one line (two blocks): 16 bytes of codes and two scale bytes.
+struct Piece {
+  g32x4 c;
+  uint32_t s;
+};
+constexpr uint32_t kOutside = 0xFFFFFFF0u;  // an offset past every buffer
+
+// The pieces of 128 values at `chunk`, whole.  off: the lane's byte offset of
+// the line's first piece; the chunk's goes into the scalar offset.
+__device__ __forceinline__ Piece load_piece(const Lines& b, uint32_t off, int chunk) {
+  Piece q;
+  q.c = __builtin_bit_cast(g32x4, __builtin_amdgcn_raw_buffer_load_b128(b.codes, (int)off, 64 * chunk, 0));
+  q.s = __builtin_amdgcn_raw_buffer_load_b16(b.scales, (int)(off / 8), 8 * chunk, 0);
+  return q;
+}
+// The same where the range ends inside the chunk, `left` values behind the
+// piece's first: blocks outside get the scale zero.
+__device__ __forceinline__ Piece load_tail(const Lines& b, uint32_t off, int chunk, int left) {
+  const uint32_t at = off + 64 * (uint32_t)chunk;
+  const uint32_t o0 = left >= 16 ? at : kOutside, o1 = left >= 32 ? at + 8 : kOutside;
+  const g32x2 lo = __builtin_bit_cast(g32x2, __builtin_amdgcn_raw_buffer_load_b64(b.codes, (int)o0, 0, 0));
+  const g32x2 hi = __builtin_bit_cast(g32x2, __builtin_amdgcn_raw_buffer_load_b64(b.codes, (int)o1, 0, 0));
+  const uint32_t s0 = __builtin_amdgcn_raw_buffer_load_b8(b.scales, (int)(left >= 16 ? at / 8 : kOutside), 0, 0);
+  const uint32_t s1 = __builtin_amdgcn_raw_buffer_load_b8(b.scales, (int)(left >= 32 ? at / 8 + 1 : kOutside), 0, 0);
+  return Piece{g32x4{lo.x, lo.y, hi.x, hi.y}, s0 | (s1 << 8)};
+}
+
 template <int GRID, bool DW, typename TC>
-__global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(GroupedParams p) {
-  __shared__ __attribute__((aligned(16))) _Float16 As[2][kTileM][kTileLd];
-  __shared__ __attribute__((aligned(16))) _Float16 Bs[2][kTileN][kTileLd];
-  __shared__ Segment seg_lds;
-  const int t = threadIdx.x, wave = t >> 6, lane = t & 63;
-  if (wave == 0) {
-    const Segment s = DW ? find_columns(p, blockIdx.z) : find_tile(p, blockIdx.x, kTileM);
-    if (lane == 0) seg_lds = s;
-  }
+__global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(GroupedParams p, TileGrid g) {
+  __shared__ __attribute__((aligned(16))) _Float16 As[2][kTileM * kLineHalves], Bs[2][kTileN * kLineHalves];
+  __shared__ Segments S;
+  const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63;
+  if (wave == 0) fill_segments<DW>(p, kTileM, S);
   __syncthreads();
-  const Segment sg = seg_lds;
-  if (sg.e < 0) return;
-  // rows of A (and C) this tile covers, and the reduction range [k0, k0 + K)
-  const int64_t m0 = DW ? (int64_t)blockIdx.y * kTileM : sg.lo;
-  const int64_t m_end = DW ? p.M : sg.hi;
-  const int64_t n0 = (int64_t)(DW ? blockIdx.x : blockIdx.y) * kTileN;
-  const bool live = DW || sg.e < p.groups;  // else rows of no segment: zeros
-  const int64_t K = live ? (DW ? sg.hi - sg.lo : p.K) : 0;
-  const int64_t ka = DW ? sg.lo : 0, kb = DW ? sg.lo : (live ? sg.e * p.b.seg_k : 0);
-  const int64_t b_line = DW || !live ? 0 : sg.e * p.b.seg_lines;
-  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 128;
-  const int lr = t >> 1, lb = 2 * (t & 1);
-  const bool a_ok = m0 + lr < m_end, b_ok = n0 + lr < p.N;
-  const int64_t ao = (a_ok ? m0 + lr : 0) * p.a.pitch + ka + 16 * lb;
-  const int64_t bo = (b_line + (b_ok ? n0 + lr : 0)) * p.b.pitch + kb + 16 * lb;
-  const uint8_t* ac = p.a.codes + ao / 2;
-  const uint8_t* as = p.a.scales + ao / 16;
-  const uint8_t* bc = p.b.codes + bo / 2;
-  const uint8_t* bs = p.b.scales + bo / 16;
-  const int nsteps = (int)((K + kTileK - 1) / kTileK);
-  struct Stage {
-    g32x4 a, b;
-    uint32_t sa, sb;
-  };
-  // two neighbouring blocks of one line: 16 bytes of codes, two scale bytes
-  // (blocks past the range are zero; a range ends on a block)
-  auto two = [&](const uint8_t* c, const uint8_t* s, bool ok, int64_t st, int64_t left, g32x4* w, uint32_t* sc) {
-    g32x4 v = {0u, 0u, 0u, 0u};
-    uint32_t q = 0;
-    const uint8_t* cp = c + st * (kTileK / 2);
-    const uint8_t* sp = s + st * (kTileK / 16);
-    if (ok && left >= 32) {
-      if (DW) {
-        const g32x2 x = *reinterpret_cast<const g32x2*>(cp), y = *reinterpret_cast<const g32x2*>(cp + 8);
-        v = g32x4{x.x, x.y, y.x, y.y};
-      } else {
-        v = *reinterpret_cast<const g32x4*>(cp);
+  // Both kinds of waves walk over the same tiles and chunks of 128 values, two
+  // steps and barriers each; step h of a chunk is in buffer h.
+  if (wave >= kConsumers) {
+    // ---- producers.  A lane holds 32 values of eight lines (every 64th), a
+    // quad of lanes 128 neighbouring values of a line (64 bytes of codes).
+    // Step h expands block h of every piece: a step's 64 values are 16 of
+    // every 32, the same ones of A and B, and a sum does not depend on its
+    // order.
+    const int q = t & 3, l0 = (t - 64 * kConsumers) >> 2;
+    const int at0 = lds_at(l0, 2 * q), at1 = lds_at(l0, 2 * q + 1);  // (the swizzle repeats every 16 lines)
+    for (uint32_t id = blockIdx.x; id < g.tiles; id += gridDim.x) {
+      const Tile T = tile_at<DW>(p, S, id, g);
+      if (T.e < 0 || T.K <= 0) continue;
+      const Lines A = lines_of(p.a, T.m0, T.m_end - T.m0, T.ka);
+      const Lines B = lines_of(p.b, T.b_line + T.n0, p.N - T.n0, T.kb);
+      uint32_t off[kPieces];
+#pragma unroll
+      for (int i = 0; i < kPieces / 2; ++i) {
+        off[i] = (uint32_t)(l0 + 64 * i) * (uint32_t)(p.a.pitch / 2) + 16 * q;
+        off[i + kPieces / 2] = (uint32_t)(b_line_of(l0) + 64 * i) * (uint32_t)(p.b.pitch / 2) + 16 * q;
       }
-      q = (uint32_t)sp[0] | ((uint32_t)sp[1] << 8);
-    } else if (ok && left >= 16) {
-      const g32x2 x = *reinterpret_cast<const g32x2*>(cp);
-      v = g32x4{x.x, x.y, 0u, 0u};
-      q = sp[0];
+      const int chunks = (T.K + 127) / 128, whole = T.K / 128;
+      auto load = [&](Piece (&v)[kPieces], int chunk) {
+        const int c = uniform(chunk);
+        if (c < whole) {
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) v[i] = load_piece(i < kPieces / 2 ? A : B, off[i], c);
+        } else if (c < chunks) {
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i)
+            v[i] = load_tail(i < kPieces / 2 ? A : B, off[i], c, T.K - 128 * c - 32 * q);
+        }
+      };
+      auto expand = [&](const Piece (&v)[kPieces]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) {
+            const f16x2 ds = expand_scales<GRID>(v[i].s);
+            const f16x2 d = h ? f16x2{ds.y, ds.y} : f16x2{ds.x, ds.x};
+            uint32_t e[8];
+            expand8_shifted<GRID>(h ? v[i].c.z : v[i].c.x, d, e);
+            expand8_shifted<GRID>(h ? v[i].c.w : v[i].c.y, d, e + 4);
+            _Float16* to = (i < kPieces / 2 ? As : Bs)[h] + 64 * (i % (kPieces / 2)) * kLineHalves;
+            *reinterpret_cast<g32x4*>(to + at0) = g32x4{e[0], e[1], e[2], e[3]};
+            *reinterpret_cast<g32x4*>(to + at1) = g32x4{e[4], e[5], e[6], e[7]};
+          }
+          __syncthreads();
+        }
+      };
+      Piece u[kPieces], v[kPieces];
+      load(u, 0);
+      for (int c = 0; c < chunks; c += 2) {
+        load(v, c + 1);
+        expand(u);
+        if (c + 1 >= chunks) break;
+        load(u, c + 2);
+        expand(v);
+      }
     }
-    *w = v;
-    *sc = q;
-  };
-  auto fetch = [&](int64_t st) {
-    Stage f;
-    const int64_t left = K - st * kTileK - 16 * lb;
-    two(ac, as, a_ok, st, left, &f.a, &f.sa);
-    two(bc, bs, b_ok, st, left, &f.b, &f.sb);
-    return f;
-  };
-  auto put = [&](const Stage& f, int buf) {
-    uint32_t e[8];
-    expand16<GRID>(g32x2{f.a.x, f.a.y}, f.sa & 0xFFu, e);
-    store16(e, &As[buf][lr][16 * lb]);
-    expand16<GRID>(g32x2{f.a.z, f.a.w}, f.sa >> 8, e);
-    store16(e, &As[buf][lr][16 * lb + 16]);
-    expand16<GRID>(g32x2{f.b.x, f.b.y}, f.sb & 0xFFu, e);
-    store16(e, &Bs[buf][lr][16 * lb]);
-    expand16<GRID>(g32x2{f.b.z, f.b.w}, f.sb >> 8, e);
-    store16(e, &Bs[buf][lr][16 * lb + 16]);
-  };
-  f32x16 acc[2][4];
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
-  Stage nxt{};
-  if (nsteps > 0) {
-    put(fetch(0), 0);
-    nxt = fetch(1);
+    __syncthreads();  // the consumers' last step
+    return;
   }
-  __syncthreads();
-  for (int st = 0; st < nsteps; ++st) {
-    const int cur = st & 1;
-    if (st + 1 < nsteps) {
-      put(nxt, cur ^ 1);
-      nxt = fetch(st + 2);
-    }
+  // ---- consumers.  At the barrier that ends a producers' step the step's
+  // buffer is complete and the other one is free again.
+  const int wm = (wave >> 1) * 64, wn = (wave & 1) * 128;
+  int fa_at[kTileK / 16], fb_at[kTileK / 16];
 #pragma unroll
-    for (int kk = 0; kk < kTileK / 16; ++kk) {
-      f16x8 fa[2], fb[4];
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-        fa[i] = *reinterpret_cast<const f16x8*>(&As[cur][wm + 32 * i + (lane & 31)][16 * kk + 8 * (lane >> 5)]);
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        fb[j] = *reinterpret_cast<const f16x8*>(&Bs[cur][wn + 32 * j + (lane & 31)][16 * kk + 8 * (lane >> 5)]);
-#pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
-    }
-    __syncthreads();
+  for (int kk = 0; kk < kTileK / 16; ++kk) {
+    const int at = lds_at(lane & 31, 2 * kk + (lane >> 5));
+    fa_at[kk] = at + wm * kLineHalves;
+    fb_at[kk] = at + wn * kLineHalves;
   }
-  const int64_t e = DW ? (int64_t)blockIdx.z : sg.e;
-  const float s = live ? p.a.ts[e] * p.b.ts[e] : 0.0f;
-  TC* c = static_cast<TC*>(p.c) + (DW ? e * p.M * p.N : 0);
+  for (uint32_t id = blockIdx.x; id < g.tiles; id += gridDim.x) {
+    const Tile T = tile_at<DW>(p, S, id, g);
+    if (T.e < 0) continue;
+    const bool busy = T.m0 + wm < T.m_end;  // the wave has rows
+    f32x16 acc[2][4];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
+      for (int j = 0; j < 4; ++j) acc[i][j] = f32x16{};
+    const int chunks = (T.K + 127) / 128;
+    for (int c = 0; c < chunks; ++c) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        __syncthreads();
+        if (!busy) continue;
+#pragma unroll
+        for (int kk = 0; kk < kTileK / 16; ++kk) {
+          f16x8 fa[2], fb[4];
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+            fa[i] = *reinterpret_cast<const f16x8*>(As[h] + fa_at[kk] + 32 * i * kLineHalves);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            fb[j] = *reinterpret_cast<const f16x8*>(Bs[h] + fb_at[kk] + 32 * j * kLineHalves);
+#pragma unroll
+          for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+        }
+      }
+    }
+    constexpr float kUnshift = (float)(1 << (2 * kExpandShift<GRID>));
+    const float s = T.live ? p.a.ts[T.e] * p.b.ts[T.e] : 0.0f;
+    const int col = T.n0 + wn + 2 * (lane & 31), row = T.m0 + wm + 4 * (lane >> 5), left = (int)p.N - col;
+    TC* c = static_cast<TC*>(p.c) + (DW ? (int64_t)T.e * p.M * p.N : 0) + (int64_t)row * p.ldc + col;
+    const int rows = T.m_end - row;
+    const bool inside = T.n0 + kTileN <= p.N;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
       for (int r = 0; r < 16; ++r) {
-        const int64_t row = m0 + wm + 32 * i + 8 * (r >> 2) + 4 * (lane >> 5) + (r & 3);
-        const int64_t col = n0 + wn + 32 * j + (lane & 31);
-        if (row < m_end && col < p.N) store_c(&c[row * p.ldc + col], acc[i][j][r] * s);
+        const int at = 32 * i + 8 * (r >> 2) + (r & 3);
+        if (at >= rows) continue;
+        TC* to = c + at * p.ldc;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float v0 = acc[i][2 * j][r] * kUnshift * s, v1 = acc[i][2 * j + 1][r] * kUnshift * s;
+          store_c(to + 64 * j, v0, v1, inside ? 2 : left - 64 * j);
+        }
       }
+  }
+  __syncthreads();
 }
 
 template <bool DW, typename TC>
-hipError_t launch_tiles(const GroupedParams& p, dim3 grid, hipStream_t s) {
+hipError_t launch_tiles(const GroupedParams& p, int64_t mt, hipStream_t s) {
+  int dev = 0, cus = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+  if (e != hipSuccess) return e;
+  const int64_t nt = (p.N + kTileN - 1) / kTileN;
+  const TileGrid g{(uint32_t)(nt * mt * (DW ? p.groups : 1)), fast_div((uint32_t)nt), fast_div((uint32_t)mt)};
+  const unsigned grid = g.tiles < (uint32_t)cus ? g.tiles : (uint32_t)cus;
   switch (p.grid) {
-    case kGridE1M2: ufp4_grouped_tile_kernel<kGridE1M2, DW, TC><<<grid, kTileThreads, 0, s>>>(p); break;
-    case kGridINT4: ufp4_grouped_tile_kernel<kGridINT4, DW, TC><<<grid, kTileThreads, 0, s>>>(p); break;
+    case kGridE1M2: ufp4_grouped_tile_kernel<kGridE1M2, DW, TC><<<grid, kTileThreads, 0, s>>>(p, g); break;
+    case kGridINT4: ufp4_grouped_tile_kernel<kGridINT4, DW, TC><<<grid, kTileThreads, 0, s>>>(p, g); break;
     case kGridE2M1:  // the clamped grid's codes are E2M1 codes
-    case kGridE2M1C: ufp4_grouped_tile_kernel<kGridE2M1, DW, TC><<<grid, kTileThreads, 0, s>>>(p); break;
+    case kGridE2M1C: ufp4_grouped_tile_kernel<kGridE2M1, DW, TC><<<grid, kTileThreads, 0, s>>>(p, g); break;
     default: return hipErrorInvalidValue;
   }
   return hipGetLastError();
@@ -232,15 +352,23 @@ hipError_t launch_tiles(const GroupedParams& p, dim3 grid, hipStream_t s) {
 
 }  // namespace
 
+// Row tiles of a launch: a segment adds at most one partial tile.
+int64_t grouped_row_tiles(const GroupedParams& p, bool dw) {
+  return dw ? (p.M + kTileM - 1) / kTileM : p.total_rows / kTileM + p.groups + 1;
+}
+
+int64_t grouped_tiles(const GroupedParams& p, bool dw) {
+  return (p.N + kTileN - 1) / kTileN * grouped_row_tiles(p, dw) * (dw ? p.groups : 1);
+}
+
 hipError_t launch_grouped_nt(const GroupedParams& p, hipStream_t s) {
-  // a segment adds at most one partial tile
-  const dim3 grid((unsigned)(p.total_rows / kTileM + p.groups + 1), (unsigned)((p.N + kTileN - 1) / kTileN));
-  return p.c_f32 ? launch_tiles<false, float>(p, grid, s) : launch_tiles<false, uint16_t>(p, grid, s);
+  const int64_t mt = grouped_row_tiles(p, false);
+  return p.c_f32 ? launch_tiles<false, float>(p, mt, s) : launch_tiles<false, uint16_t>(p, mt, s);
 }
 
 hipError_t launch_grouped_dw(const GroupedParams& p, hipStream_t s) {
-  const dim3 grid((unsigned)((p.N + kTileN - 1) / kTileN), (unsigned)((p.M + kTileM - 1) / kTileM), (unsigned)p.groups);
-  return p.c_f32 ? launch_tiles<true, float>(p, grid, s) : launch_tiles<true, uint16_t>(p, grid, s);
+  const int64_t mt = grouped_row_tiles(p, true);
+  return p.c_f32 ? launch_tiles<true, float>(p, mt, s) : launch_tiles<true, uint16_t>(p, mt, s);
 }
 
 }  // namespace ufp4

@@ -130,6 +130,8 @@ struct GroupedParams {
   void* c;
   int64_t ldc;
 };
+// 256 x 256 tiles of a call's grid (a launch takes fewer than 2^31).
+int64_t grouped_tiles(const GroupedParams& p, bool dw);
 hipError_t launch_grouped_nt(const GroupedParams& p, hipStream_t s);
 hipError_t launch_grouped_dw(const GroupedParams& p, hipStream_t s);
 

@@ -289,7 +289,7 @@ int ufp4_gemm_grouped_nt(const ufp4_config* cfg, int64_t total_rows, int64_t N, 
   if (total_rows < 0 || N < 0 || K < 0 || ldc < N || num_groups < 1 || num_groups > 1024 || !type_ok(c_type) ||
       (b_layout != 0 && b_layout != 1))
     return UFP4_ERR_INVALID_ARGUMENT;
-  if (K % 32 || K >= kMaxDim || (N + 255) / 256 > kMaxTiles || total_rows >= kMaxDim) return UFP4_ERR_SHAPE;
+  if (K % 32 || K >= kMaxDim || (b_layout == 1 && K * num_groups >= kMaxDim) || (N + 255) / 256 > kMaxTiles || total_rows >= kMaxDim) return UFP4_ERR_SHAPE;
   if (total_rows == 0 || N == 0) return UFP4_OK;
   if (!c || !offsets_dev) return UFP4_ERR_INVALID_ARGUMENT;
   if ((rc = grouped_operand(a, 16, K == 0)) || (rc = grouped_operand(b, 16, K == 0))) return rc;
@@ -306,6 +306,7 @@ int ufp4_gemm_grouped_nt(const ufp4_config* cfg, int64_t total_rows, int64_t N, 
   p.K = K;
   p.c = c;
   p.ldc = ldc;
+  if (grouped_tiles(p, false) >> 31) return UFP4_ERR_SHAPE;
   return done(launch_grouped_nt(p, (hipStream_t)stream));
 }
 
@@ -334,6 +335,7 @@ int ufp4_gemm_grouped_dw(const ufp4_config* cfg, int64_t M, int64_t N, int64_t p
   p.N = N;
   p.c = c;
   p.ldc = N;
+  if (grouped_tiles(p, true) >> 31) return UFP4_ERR_SHAPE;
   return done(launch_grouped_dw(p, (hipStream_t)stream));
 }
 

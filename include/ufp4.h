@@ -459,9 +459,10 @@ int ufp4_gated_act_backward(const uint16_t* dh, int64_t lddh, const uint8_t* cod
  * num_groups floats.  offsets_dev: num_groups + 1 int64 (more may follow),
  * 1 <= num_groups <= 1024, offsets[0] counts as 0; rows behind the last
  * segment get zeros, and offsets are clamped to [0, total_rows].  c of c_type, leading dimension ldc >= N.
- * Sums in fp32 of exact products, rounded once.  K % 32 == 0, K and total_rows
- * below 2^25, N at most 65535 * 256 (UFP4_ERR_SHAPE); codes 16-byte aligned,
- * block scales 2-byte aligned. */
+ * Sums in fp32 of exact products, rounded once.  K % 32 == 0; K, total_rows
+ * and the length of b's lines below 2^25, as the quantizer writes them; N at
+ * most 65535 * 256 (UFP4_ERR_SHAPE); codes 16-byte aligned, block scales
+ * 2-byte aligned. */
 int ufp4_gemm_grouped_nt(const ufp4_config* cfg, int64_t total_rows, int64_t N, int64_t K, ufp4_qtensor a,
                          ufp4_qtensor b, int32_t b_layout, const int64_t* offsets_dev, int32_t num_groups, void* c,
                          int32_t c_type, int64_t ldc, ufp4_stream_t stream);
