@@ -27,9 +27,10 @@ constexpr int kPieces = (kTileM + kTileN) / (16 * kProducers);  // per producer 
 // LDS: [A, B][buffer][line][64 fp16] (both buffers of an operand inside the
 // 16-bit offset of an LDS instruction).  The eight 16-byte chunks of a line are stored in the order chunk ^ swizzle(line):
 // the same chunk of neighbouring lines (a fragment load) and neighbouring
-// chunks of a line (an expansion store) then fall on different banks.
+// chunks of a line (an expansion store of two lines) then fall on different
+// banks.
 constexpr int kLineHalves = kTileK;
-__device__ __forceinline__ int swizzle(int line) { return (line >> 1) & 7; }
+__device__ __forceinline__ int swizzle(int line) { return ((line >> 1) & 7) ^ (line & 1); }
 __device__ __forceinline__ int lds_at(int line, int chunk) { return line * kLineHalves + 8 * (chunk ^ swizzle(line)); }
 
 // A value that all lanes of the wave hold, as a scalar: branches, loop counts
