@@ -21,6 +21,8 @@ namespace {
 // other waves instead of between it.  All waves meet in one barrier per step.
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
 constexpr int kConsumers = 8, kProducers = 4;
+constexpr uint32_t kXcds = 8;
+constexpr int64_t kXcdRows = 32;
 constexpr int kTileThreads = 64 * (kConsumers + kProducers);
 constexpr int kPieces = (kTileM + kTileN) / (16 * kProducers);  // per producer lane
 
@@ -135,17 +137,23 @@ struct Tile {
   int32_t m0, m_end, n0, K, ka;
   int64_t kb, b_line;
 };
-// Tile ids: column tiles innermost, then row tiles, then (dw) groups.
+// Tile ids.  The tiles of one row of tiles (`nt` of them) share a panel of A.
+// Workgroups are dealt to the XCDs in turn, so id % 8 is the XCD: rows of tiles
+// go to XCDs in turn and a row's tiles stay on its XCD, whose L2 then reads the
+// panel once.  With few rows the ids are the tiles in order.
 struct TileGrid {
-  uint32_t tiles;
-  FastDiv nt, mt;
+  uint32_t ids;
+  FastDiv nt, mt;  // column tiles; row tiles a group (dw)
+  int32_t xcd;
 };
 template <bool DW>
 __device__ __forceinline__ Tile tile_at(const GroupedParams& p, const Segments& S, uint32_t id, const TileGrid& g) {
-  const uint32_t row = g.nt.div(id);
-  const int32_t n0 = (int32_t)(id - row * g.nt.d) * kTileN;
+  const uint32_t l = g.xcd ? id / kXcds : id, q = g.nt.div(l);
+  const uint32_t row = g.xcd ? q * kXcds + id % kXcds : q;
+  const int32_t n0 = (int32_t)(l - q * g.nt.d) * kTileN;
   if (DW) {
     const uint32_t e = g.mt.div(row);
+    if (e >= (uint32_t)p.groups) return Tile{-1, false, 0, 0, 0, 0, 0, 0, 0};
     const int lo = uniform(S.lo[e]), hi = uniform(S.hi[e]);
     return Tile{(int32_t)e, true, (int32_t)(row - e * g.mt.d) * kTileM, (int32_t)p.M, n0, hi - lo, lo, lo, 0};
   }
@@ -214,7 +222,7 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
     // order.
     const int q = t & 3, l0 = (t - 64 * kConsumers) >> 2;
     const int at0 = lds_at(l0, 2 * q), at1 = lds_at(l0, 2 * q + 1);  // (the swizzle repeats every 16 lines)
-    for (uint32_t id = blockIdx.x; id < g.tiles; id += gridDim.x) {
+    for (uint32_t id = blockIdx.x; id < g.ids; id += gridDim.x) {
       const Tile T = tile_at<DW>(p, S, id, g);
       if (T.e < 0 || T.K <= 0) continue;
       const Lines A = lines_of(p.a, T.m0, T.m_end - T.m0, T.ka);
@@ -277,7 +285,7 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
     fa_at[kk] = at + wm * kLineHalves;
     fb_at[kk] = at + wn * kLineHalves;
   }
-  for (uint32_t id = blockIdx.x; id < g.tiles; id += gridDim.x) {
+  for (uint32_t id = blockIdx.x; id < g.ids; id += gridDim.x) {
     const Tile T = tile_at<DW>(p, S, id, g);
     if (T.e < 0) continue;
     const bool busy = T.m0 + wm < T.m_end;  // the wave has rows
@@ -339,8 +347,11 @@ hipError_t launch_tiles(const GroupedParams& p, int64_t mt, hipStream_t s) {
   if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
   if (e != hipSuccess) return e;
   const int64_t nt = (p.N + kTileN - 1) / kTileN;
-  const TileGrid g{(uint32_t)(nt * mt * (DW ? p.groups : 1)), fast_div((uint32_t)nt), fast_div((uint32_t)mt)};
-  const unsigned grid = g.tiles < (uint32_t)cus ? g.tiles : (uint32_t)cus;
+  const int64_t rows = mt * (DW ? p.groups : 1);
+  const bool xcd = rows >= kXcdRows && cus % kXcds == 0;
+  const int64_t ids = nt * (xcd ? (rows + kXcds - 1) / kXcds * kXcds : rows);
+  const TileGrid g{(uint32_t)ids, fast_div((uint32_t)nt), fast_div((uint32_t)mt), xcd};
+  const unsigned grid = g.ids < (uint32_t)cus ? g.ids : (uint32_t)cus;
   switch (p.grid) {
     case kGridE1M2: ufp4_grouped_tile_kernel<kGridE1M2, DW, TC><<<grid, kTileThreads, 0, s>>>(p, g); break;
     case kGridINT4: ufp4_grouped_tile_kernel<kGridINT4, DW, TC><<<grid, kTileThreads, 0, s>>>(p, g); break;
