@@ -340,18 +340,190 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
   __syncthreads();
 }
 
-template <bool DW, typename TC>
-hipError_t launch_tiles(const GroupedParams& p, int64_t mt, hipStream_t s) {
+// ------------------------------------------------------------- few rows
+// Products with few rows a segment read the segment's matrix once and are
+// bound by that.  A workgroup takes 16 NT lines of B and up to 16 MT rows of a
+// segment; its four waves take the reduction's stretches of 512 values in turn
+// and their sums are added in LDS in a fixed order.  Operands go from memory to
+// registers: a lane holds 128 neighbouring values of a line (its codes four
+// 16-byte loads, its scales one of 8 bytes), the four lane groups of the MFMA
+// 512 of the line.  The MFMA's 32 values are then 8 of each group's, the same
+// ones of both operands, so nothing is exchanged between lanes.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+constexpr int kRowWaves = 4, kRowThreads = 64 * kRowWaves, kStretch = 512;
+
+// 128 values of a line: codes and scales of its eight blocks.
+struct Stretch {
+  g32x4 c[4];
+  g32x2 s;
+};
+// off: byte offset of the lane's first code in `stretch` 0.  whole: the stretch
+// is inside the range; else `left` values of the lane's are (whole pieces of
+// 32; the others read as code and scale zero).
+__device__ __forceinline__ Stretch load_stretch(const Lines& b, uint32_t off, int stretch, bool whole, int left) {
+  Stretch v;
+  if (whole) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      v.c[i] = __builtin_bit_cast(g32x4, __builtin_amdgcn_raw_buffer_load_b128(b.codes, (int)(off + 16 * i), 256 * stretch, 0));
+    v.s = __builtin_bit_cast(g32x2, __builtin_amdgcn_raw_buffer_load_b64(b.scales, (int)(off / 8), 32 * stretch, 0));
+  } else {
+    const uint32_t at = off + 256 * (uint32_t)stretch;
+    uint32_t s[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const bool in = 32 * i < left;
+      v.c[i] = __builtin_bit_cast(g32x4, __builtin_amdgcn_raw_buffer_load_b128(b.codes, (int)(in ? at + 16 * i : kOutside), 0, 0));
+      s[i] = __builtin_amdgcn_raw_buffer_load_b16(b.scales, (int)(in ? at / 8 + 2 * i : kOutside), 0, 0);
+    }
+    v.s = g32x2{s[0] | (s[1] << 16), s[2] | (s[3] << 16)};
+  }
+  return v;
+}
+// Piece i (32 values) as four MFMA fragments.
+template <int GRID>
+__device__ __forceinline__ void expand_piece(const Stretch& v, int i, f16x8 (&f)[4]) {
+  const f16x2 ds = expand_scales<GRID>((i < 2 ? v.s.x : v.s.y) >> (16 * (i & 1)));
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t e[4];
+    expand8_shifted<GRID>(v.c[i][j], j < 2 ? f16x2{ds.x, ds.x} : f16x2{ds.y, ds.y}, e);
+    f[j] = __builtin_bit_cast(f16x8, g32x4{e[0], e[1], e[2], e[3]});
+  }
+}
+
+// The row tile `tile` straight from the offsets, by each wave for itself.
+__device__ __forceinline__ RowTile find_tile(const GroupedParams& p, int tile, int rows) {
+  const int lane = threadIdx.x & 63;
+  int before = 0;
+  for (int e0 = 0; e0 <= p.groups; e0 += 64) {
+    const int e = e0 + lane < p.groups ? e0 + lane : p.groups;
+    int64_t lo, hi;
+    segment_rows(p, e, &lo, &hi);
+    if (e0 + lane > p.groups) hi = lo;
+    const int n = (int)((hi - lo + rows - 1) / rows);
+    int inc = n;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+      const int o = __shfl_up(inc, d);
+      if (lane >= d) inc += o;
+    }
+    const int first = before + inc - n;
+    const uint64_t hit = __ballot(tile >= first && tile < first + n);
+    if (hit) {
+      const int src = __ffsll((unsigned long long)hit) - 1;
+      const int from = uniform(__shfl((int)lo + (tile - first) * rows, src)), end = uniform(__shfl((int)hi, src));
+      return RowTile{uniform(__shfl(e, src)), from, from + rows < end ? from + rows : end};
+    }
+    before += uniform(__shfl(inc, 63));
+  }
+  return RowTile{-1, 0, 0};
+}
+
+// Four neighbouring values of a row of C, n of them inside it.
+__device__ __forceinline__ void store_c4(float* c, const f32x4& v, int n) {
+  store_c(c, v[0], v[1], n);
+  store_c(c + 2, v[2], v[3], n - 2);
+}
+__device__ __forceinline__ void store_c4(uint16_t* c, const f32x4& v, int n) {
+  if (n >= 4) {
+    store_8<2>(c, v32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
+  } else {
+    store_c(c, v[0], v[1], n);
+    store_c(c + 2, v[2], v[3], n - 2);
+  }
+}
+
+template <int GRID, int MT, int NT, typename TC>
+__global__ __launch_bounds__(kRowThreads) void ufp4_grouped_rows_kernel(GroupedParams p, FastDiv nt) {
+  __shared__ f32x4 part[kRowWaves][MT * NT][64];
+  const int t = threadIdx.x, wave = uniform(t >> 6), lane = t & 63, g = lane >> 4, r = lane & 15;
+  const uint32_t tile = nt.div(blockIdx.x);
+  const int n0 = (int)(blockIdx.x - tile * nt.d) * 16 * NT;
+  const RowTile T = find_tile(p, (int)tile, 16 * MT);
+  if (T.e < 0) return;
+  const bool live = T.e < p.groups;
+  f32x4 acc[MT][NT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) acc[m][n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  if (live) {
+    const int K = (int)p.K;
+    const Lines A = lines_of(p.a, T.lo, T.hi - T.lo, 0);
+    const Lines B = lines_of(p.b, T.e * p.b.seg_lines + n0, p.N - n0, T.e * p.b.seg_k);
+    const uint32_t pa = (uint32_t)(p.a.pitch / 2), pb = (uint32_t)(p.b.pitch / 2);
+    for (int c = wave; c * kStretch < K; c += kRowWaves) {
+      const bool whole = (c + 1) * kStretch <= K;
+      const int left = K - c * kStretch - 128 * g;
+      Stretch a[MT], b[NT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) b[n] = load_stretch(B, (uint32_t)(16 * n + r) * pb + 64 * g, c, whole, left);
+#pragma unroll
+      for (int m = 0; m < MT; ++m) a[m] = load_stretch(A, (uint32_t)(16 * m + r) * pa + 64 * g, c, whole, left);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        f16x8 fa[MT][4];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) expand_piece<GRID>(a[m], i, fa[m]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          f16x8 fb[4];
+          expand_piece<GRID>(b[n], i, fb);
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              acc[m][n] = __builtin_amdgcn_mfma_f32_16x16x32_f16(fb[j], fa[m][j], acc[m][n], 0, 0, 0);
+        }
+      }
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) part[wave][m * NT + n][lane] = acc[m][n];
+  __syncthreads();
+  constexpr float kUnshift = (float)(1 << (2 * kExpandShift<GRID>));
+  const float s = live ? p.a.ts[T.e] * p.b.ts[T.e] : 0.0f;
+  for (int i = wave; i < MT * NT; i += kRowWaves) {
+    f32x4 v = part[0][i][lane];
+#pragma unroll
+    for (int w = 1; w < kRowWaves; ++w) v += part[w][i][lane];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) v[k] = v[k] * kUnshift * s;
+    // a lane holds row r of the 16 and four neighbouring columns
+    const int row = T.lo + 16 * (i / NT) + r, col = n0 + 16 * (i % NT) + 4 * g;
+    if (row < T.hi && col < p.N)
+      store_c4(static_cast<TC*>(p.c) + (int64_t)row * p.ldc + col, v, (int)(p.N - col < 4 ? p.N - col : 4));
+  }
+}
+
+// Compute units of the current device.
+hipError_t compute_units(int64_t* out) {
   int dev = 0, cus = 0;
   hipError_t e = hipGetDevice(&dev);
   if (e == hipSuccess) e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-  if (e != hipSuccess) return e;
-  const int64_t nt = (p.N + kTileN - 1) / kTileN;
-  const int64_t rows = mt * (DW ? p.groups : 1);
+  *out = cus;
+  return e;
+}
+
+// Row tiles of a launch: every segment that has rows adds at most one partial
+// tile, and so do the rows behind the last one.
+int64_t segment_tiles(const GroupedParams& p, int rows) {
+  return p.total_rows / rows + (p.groups < p.total_rows ? p.groups : p.total_rows) + 1;
+}
+int64_t row_tiles(const GroupedParams& p, bool dw) {
+  return dw ? (p.M + kTileM - 1) / kTileM : segment_tiles(p, kTileM);
+}
+
+template <bool DW, typename TC>
+hipError_t launch_tiles(const GroupedParams& p, int64_t cus, hipStream_t s) {
+  const int64_t nt = (p.N + kTileN - 1) / kTileN, mt = row_tiles(p, DW), rows = mt * (DW ? p.groups : 1);
   const bool xcd = rows >= kXcdRows && cus % kXcds == 0;
   const int64_t ids = nt * (xcd ? (rows + kXcds - 1) / kXcds * kXcds : rows);
   const TileGrid g{(uint32_t)ids, fast_div((uint32_t)nt), fast_div((uint32_t)mt), xcd};
-  const unsigned grid = g.ids < (uint32_t)cus ? g.ids : (uint32_t)cus;
+  const unsigned grid = (unsigned)(ids < cus ? ids : cus);
   switch (p.grid) {
     case kGridE1M2: ufp4_grouped_tile_kernel<kGridE1M2, DW, TC><<<grid, kTileThreads, 0, s>>>(p, g); break;
     case kGridINT4: ufp4_grouped_tile_kernel<kGridINT4, DW, TC><<<grid, kTileThreads, 0, s>>>(p, g); break;
@@ -362,25 +534,70 @@ hipError_t launch_tiles(const GroupedParams& p, int64_t mt, hipStream_t s) {
   return hipGetLastError();
 }
 
-}  // namespace
-
-// Row tiles of a launch: a segment adds at most one partial tile.
-int64_t grouped_row_tiles(const GroupedParams& p, bool dw) {
-  return dw ? (p.M + kTileM - 1) / kTileM : p.total_rows / kTileM + p.groups + 1;
+template <int MT, int NT, typename TC>
+hipError_t launch_rows(const GroupedParams& p, hipStream_t s) {
+  const int64_t nt = (p.N + 16 * NT - 1) / (16 * NT);
+  const unsigned grid = (unsigned)(nt * segment_tiles(p, 16 * MT));
+  const FastDiv d = fast_div((uint32_t)nt);
+  switch (p.grid) {
+    case kGridE1M2: ufp4_grouped_rows_kernel<kGridE1M2, MT, NT, TC><<<grid, kRowThreads, 0, s>>>(p, d); break;
+    case kGridINT4: ufp4_grouped_rows_kernel<kGridINT4, MT, NT, TC><<<grid, kRowThreads, 0, s>>>(p, d); break;
+    case kGridE2M1:
+    case kGridE2M1C: ufp4_grouped_rows_kernel<kGridE2M1, MT, NT, TC><<<grid, kRowThreads, 0, s>>>(p, d); break;
+    default: return hipErrorInvalidValue;
+  }
+  return hipGetLastError();
 }
 
+// The kernel of an nt call.  Measured with 64 segments, N = K = 4096 (us): 2
+// rows a segment 111 (16 rows a workgroup), 133 (32 rows), 248 (tiles); 8 rows
+// 134, 162, 253; 16 rows 184, 174, 258; 32 rows 280, 231, 263; 64 rows 457,
+// 374, 300; 128 rows 834, 659, 407.  One segment, N = K = 2048: 500 rows 20, 14,
+// 42 (16 tiles leave most of the device idle).  So a round of tiles, one a
+// compute unit, costs what about 11 workgroups of 32 rows a compute unit do.  A
+// segment is taken to end in the middle of a tile.  Half as many lines a
+// workgroup pay where there are few workgroups: 24 segments of 4 rows, N 1000, K
+// 2080: 13.2 (32 lines) against 16.3 us (64); 64 segments of 8 rows, N = K =
+// 4096: 144 against 136.
+enum RowsKernel { kTiles, kRows16Lines32, kRows16Lines64, kRows32Lines64 };
+RowsKernel rows_kernel(const GroupedParams& p, int64_t cus) {
+  const int64_t nt = (p.N + 63) / 64, ends = p.groups < p.total_rows ? p.groups : p.total_rows;
+  if (2 * nt * segment_tiles(p, 16) >= ((int64_t)1 << 24)) return kTiles;  // (threads of a launch)
+  const int64_t wgs = (p.total_rows / 32 + (ends + 1) / 2) * nt;
+  const int64_t tiles = (p.total_rows / kTileM + (ends + 1) / 2) * ((p.N + kTileN - 1) / kTileN);
+  if (wgs >= 11 * cus * ((tiles + cus - 1) / cus)) return kTiles;
+  if (p.total_rows > 12 * p.groups) return kRows32Lines64;
+  return wgs < 2 * cus ? kRows16Lines32 : kRows16Lines64;
+}
+
+template <typename TC>
+hipError_t launch_nt(const GroupedParams& p, hipStream_t s) {
+  int64_t cus = 0;
+  const hipError_t e = compute_units(&cus);
+  if (e != hipSuccess) return e;
+  switch (rows_kernel(p, cus)) {
+    case kRows16Lines32: return launch_rows<1, 2, TC>(p, s);
+    case kRows16Lines64: return launch_rows<1, 4, TC>(p, s);
+    case kRows32Lines64: return launch_rows<2, 4, TC>(p, s);
+    default: return launch_tiles<false, TC>(p, cus, s);
+  }
+}
+
+}  // namespace
+
 int64_t grouped_tiles(const GroupedParams& p, bool dw) {
-  return (p.N + kTileN - 1) / kTileN * grouped_row_tiles(p, dw) * (dw ? p.groups : 1);
+  return (p.N + kTileN - 1) / kTileN * (row_tiles(p, dw) * (dw ? p.groups : 1) + kXcds);
 }
 
 hipError_t launch_grouped_nt(const GroupedParams& p, hipStream_t s) {
-  const int64_t mt = grouped_row_tiles(p, false);
-  return p.c_f32 ? launch_tiles<false, float>(p, mt, s) : launch_tiles<false, uint16_t>(p, mt, s);
+  return p.c_f32 ? launch_nt<float>(p, s) : launch_nt<uint16_t>(p, s);
 }
 
 hipError_t launch_grouped_dw(const GroupedParams& p, hipStream_t s) {
-  const int64_t mt = grouped_row_tiles(p, true);
-  return p.c_f32 ? launch_tiles<true, float>(p, mt, s) : launch_tiles<true, uint16_t>(p, mt, s);
+  int64_t cus = 0;
+  const hipError_t e = compute_units(&cus);
+  if (e != hipSuccess) return e;
+  return p.c_f32 ? launch_tiles<true, float>(p, cus, s) : launch_tiles<true, uint16_t>(p, cus, s);
 }
 
 }  // namespace ufp4

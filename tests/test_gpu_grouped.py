@@ -118,6 +118,14 @@ def test_nt_narrow(env, N):
     run_nt(env, [3, 300], N, 96, E2M1, 0, True, N)
 
 
+@pytest.mark.parametrize("counts", [[1500, 0, 255, 257, 3200, 1, 700], [5900, 0], [40, 256, 512, 4700, 300]],
+                         ids=["ragged", "one segment", "whole tiles"])
+@pytest.mark.parametrize("layout", [0, 1])
+@pytest.mark.parametrize("N,K,grid", [(1030, 160, E1M2), (1024, 128, INT4), (1023, 32, E2M1), (1280, 640, E1M2)])
+def test_nt_many_rows(env, counts, layout, N, K, grid):
+    run_nt(env, counts, N, K, grid, layout, N % 2 == 0, N + K + layout, spare=5, ldc_pad=3)
+
+
 def test_nt_no_reduction_and_no_rows(env):
     run_nt(env, [3, 4], 20, 0, E1M2, 0, False, 1)
     run_nt(env, [0, 0], 20, 32, E1M2, 0, False, 1)
