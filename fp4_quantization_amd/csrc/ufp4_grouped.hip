@@ -322,7 +322,18 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
     const int col = T.n0 + wn + 2 * (lane & 31), row = T.m0 + wm + 4 * (lane >> 5), left = (int)p.N - col;
     TC* c = static_cast<TC*>(p.c) + (DW ? (int64_t)T.e * p.M * p.N : 0) + (int64_t)row * p.ldc + col;
     const int rows = T.m_end - row;
-    const bool inside = T.n0 + kTileN <= p.N;
+    const float s2 = kUnshift * s;
+    if (T.n0 + kTileN <= p.N && T.m0 + wm + 64 <= T.m_end) {  // (the wave's part is inside C)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          TC* to = c + (32 * i + 8 * (r >> 2) + (r & 3)) * p.ldc;
+          store_c(to, acc[i][0][r] * s2, acc[i][1][r] * s2, 2);
+          store_c(to + 64, acc[i][2][r] * s2, acc[i][3][r] * s2, 2);
+        }
+      continue;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -330,11 +341,8 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
         const int at = 32 * i + 8 * (r >> 2) + (r & 3);
         if (at >= rows) continue;
         TC* to = c + at * p.ldc;
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const float v0 = acc[i][2 * j][r] * kUnshift * s, v1 = acc[i][2 * j + 1][r] * kUnshift * s;
-          store_c(to + 64 * j, v0, v1, inside ? 2 : left - 64 * j);
-        }
+        store_c(to, acc[i][0][r] * s2, acc[i][1][r] * s2, left);
+        store_c(to + 64, acc[i][2][r] * s2, acc[i][3][r] * s2, left - 64);
       }
   }
   __syncthreads();
