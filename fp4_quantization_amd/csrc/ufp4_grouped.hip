@@ -114,6 +114,12 @@ __device__ __forceinline__ void store_c(float* c, float v0, float v1, int n) {
   else if (n == 1)
     *c = v0;
 }
+// The same inside C, past the caches: the weight gradients of a step are larger
+// than them (64 experts, 4096 x 2048, fp32: 1270 us through them, 1134 past).
+typedef float f32x2s __attribute__((ext_vector_type(2), aligned(4)));
+__device__ __forceinline__ void stream_c(float* c, float v0, float v1) {
+  __builtin_nontemporal_store(f32x2s{v0, v1}, reinterpret_cast<f32x2s*>(c));
+}
 struct __attribute__((packed, aligned(2))) Pair16 {
   uint32_t w;
 };
@@ -123,6 +129,7 @@ __device__ __forceinline__ void store_c(uint16_t* c, float v0, float v1, int n) 
   else if (n == 1)
     *c = to_bf16(v0);
 }
+__device__ __forceinline__ void stream_c(uint16_t* c, float v0, float v1) { store_c(c, v0, v1, 2); }
 
 // The line of B (of each 64) that LDS row r holds: columns 2 i and 2 i + 1 of
 // C come from the same lane of two neighbouring column tiles of 32, so a lane
@@ -329,8 +336,8 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
           TC* to = c + (32 * i + 8 * (r >> 2) + (r & 3)) * p.ldc;
-          store_c(to, acc[i][0][r] * s2, acc[i][1][r] * s2, 2);
-          store_c(to + 64, acc[i][2][r] * s2, acc[i][3][r] * s2, 2);
+          stream_c(to, acc[i][0][r] * s2, acc[i][1][r] * s2);
+          stream_c(to + 64, acc[i][2][r] * s2, acc[i][3][r] * s2);
         }
       continue;
     }
