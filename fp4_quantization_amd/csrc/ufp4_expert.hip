@@ -23,7 +23,7 @@ namespace {
 // Up to kSortSingle slots one workgroup does all three in one launch.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortBlocks = 64;
-constexpr int kSortSingle = 4096;
+constexpr int kSortSingle = 5120;  // (one launch 9.7 us at 4000 slots, 15.6 at 8192; three launches 12 to 13)
 constexpr int kSortMaxE = kMaxExperts + 1;  // + the key of dropped slots
 
 __device__ __forceinline__ int sort_key(const SortParams& p, int s) {
@@ -151,18 +151,24 @@ __global__ __launch_bounds__(kSortThreads) void ufp4_sort_count_kernel(SortParam
   if (t < p.experts) p.row_of_slot[s0 + t] = cnt[t];
 }
 
+// (a thread holds its expert's counts of all blocks, read together)
 __global__ __launch_bounds__(kSortThreads) void ufp4_sort_scan_kernel(SortParams p, int per, int blocks) {
   __shared__ int wsum[kSortWaves];
   const int t = threadIdx.x;
-  int count = 0;
-  if (t < p.experts)
-    for (int b = 0; b < blocks; ++b) count += p.row_of_slot[b * per + t];
+  int n[kSortBlocks], count = 0;
+  const int32_t* mine = p.row_of_slot + (t < p.experts ? t : p.experts - 1);
+#pragma unroll
+  for (int b = 0; b < kSortBlocks; ++b) n[b] = mine[(b < blocks ? b : blocks - 1) * per];  // (in bounds, no branches)
+#pragma unroll
+  for (int b = 0; b < kSortBlocks; ++b) n[b] = t < p.experts && b < blocks ? n[b] : 0;
+#pragma unroll
+  for (int b = 0; b < kSortBlocks; ++b) count += n[b];
   int at = sort_offsets(p, count, wsum);
-  if (t < p.experts)
-    for (int b = 0; b < blocks; ++b) {
-      const int n = p.row_of_slot[b * per + t];
+#pragma unroll
+  for (int b = 0; b < kSortBlocks; ++b)
+    if (t < p.experts && b < blocks) {
       p.row_of_slot[b * per + t] = at;
-      at += n;
+      at += n[b];
     }
 }
 
@@ -215,7 +221,8 @@ __device__ void zero_padding(const int32_t* slot_of_row, int64_t slots_total, in
   }
 }
 
-template <int FMT>
+// S: stores past the caches.
+template <int FMT, bool S>
 __global__ __launch_bounds__(kRowThreads) void ufp4_dispatch_kernel(DispatchParams p, int64_t t0, uint32_t items,
                                                                     uint32_t item_wgs, FastDiv lanes) {
   if (blockIdx.x >= item_wgs) {
@@ -233,14 +240,14 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_dispatch_kernel(DispatchPara
   const int32_t* rs = p.row_of_slot + t * p.slots;
   for (int j = 0; j < p.slots; ++j) {
     const int32_t r = rs[j];
-    if (r >= 0 && r < p.total_rows) row_store_bits(p.out + (int64_t)r * p.ldo + col, w, n);
+    if (r >= 0 && r < p.total_rows) row_store_bits<S>(p.out + (int64_t)r * p.ldo + col, w, n);
   }
 }
 
 // --------------------------------------------------------------- combine
 // An item is eight columns of a token: the rows of its slots are read and
 // summed in slot order in fp32.  Bound by the loads of z.
-template <typename TZ, typename TO>
+template <typename TZ, typename TO, bool S>
 __global__ __launch_bounds__(kRowThreads) void ufp4_combine_kernel(CombineParams p, int64_t t0, uint32_t items,
                                                                    FastDiv lanes) {
   const uint32_t i = blockIdx.x * kRowThreads + threadIdx.x;
@@ -255,11 +262,11 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_combine_kernel(CombineParams
     const int32_t r = rs[j];
     if (r < 0 || r >= p.total_rows) continue;
     const float w = p.weights ? p.weights[t * p.slots + j] : 1.0f;
-    const V8 z = row_load(static_cast<const TZ*>(p.z) + (int64_t)r * p.ldz + col, n);
+    const V8 z = row_load<S>(static_cast<const TZ*>(p.z) + (int64_t)r * p.ldz + col, n);
 #pragma unroll
     for (int k = 0; k < 8; ++k) acc.v[k] = __builtin_fmaf(w, z.v[k], acc.v[k]);
   }
-  row_store(static_cast<TO*>(p.out) + t * p.ldo + col, acc, n);
+  row_store<S>(static_cast<TO*>(p.out) + t * p.ldo + col, acc, n);
 }
 
 // ------------------------------------------------------ combine's gradient
@@ -268,7 +275,7 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_combine_kernel(CombineParams
 // sums a lane, summed over lanes in a fixed order) and their rows of dz.
 constexpr int kBwdSlots = 8;
 
-template <typename TD, typename TZ, int THREADS>
+template <typename TD, typename TZ, int THREADS, bool S>
 __global__ __launch_bounds__(kRowThreads) void ufp4_combine_bwd_kernel(CombineBwdParams p, int64_t t0,
                                                                        uint32_t item_wgs) {
   __shared__ float part[kRowThreads / 64][kBwdSlots];
@@ -300,7 +307,7 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_combine_bwd_kernel(CombineBw
         for (int j = 0; j < kBwdSlots; ++j) {
           if (row[j] < 0) continue;
           if (p.dw) {
-            const V8 z = row_load(static_cast<const TZ*>(p.z) + (int64_t)row[j] * p.ldz + col, n);
+            const V8 z = row_load<S>(static_cast<const TZ*>(p.z) + (int64_t)row[j] * p.ldz + col, n);
 #pragma unroll
             for (int k = 0; k < 8; ++k) dot[j] = __builtin_fmaf(d.v[k], z.v[k], dot[j]);
           }
@@ -308,7 +315,7 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_combine_bwd_kernel(CombineBw
             V8 o;
 #pragma unroll
             for (int k = 0; k < 8; ++k) o.v[k] = w[j] * d.v[k];
-            row_store(static_cast<TZ*>(p.dz) + (int64_t)row[j] * p.lddz + col, o, n);
+            row_store<S>(static_cast<TZ*>(p.dz) + (int64_t)row[j] * p.lddz + col, o, n);
           }
         }
       }
@@ -344,7 +351,12 @@ uint32_t pad_wgs(int64_t rows) {
 constexpr int64_t kMaxRowItems = (int64_t)1 << 30;
 constexpr int64_t kMaxBwdTokens = (int64_t)1 << 22;  // at most one workgroup each in a launch
 
-template <int FMT>
+// Calls that move more than the last-level cache holds go past the caches:
+// 8192 tokens of 4096 to 8 of 64 experts (612 MB) 128 -> 112 us (the loads stay
+// cached: with them past it 125), the combination back 124 -> 111, its gradient
+// (1.1 GB) 239 -> 233; half as many tokens or fewer are as fast or faster with
+// the caches.
+template <int FMT, bool S>
 hipError_t dispatch(const DispatchParams& p, hipStream_t s) {
   const int64_t lanes = (p.cols + 7) / 8, step = kMaxRowItems / lanes;
   // slices of at most 2^30 items (31-bit item indices); the padding rows go
@@ -354,14 +366,14 @@ hipError_t dispatch(const DispatchParams& p, hipStream_t s) {
     const uint32_t items = (uint32_t)(n * lanes), wgs = (items + kRowThreads - 1) / kRowThreads;
     const uint32_t all = wgs + (t0 == 0 ? pad_wgs(p.total_rows) : 0);
     if (!all) return hipSuccess;
-    ufp4_dispatch_kernel<FMT><<<all, kRowThreads, 0, s>>>(p, t0, items, wgs, fast_div((uint32_t)lanes));
+    ufp4_dispatch_kernel<FMT, S><<<all, kRowThreads, 0, s>>>(p, t0, items, wgs, fast_div((uint32_t)lanes));
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
 }
 
-template <typename TD, typename TZ>
+template <typename TD, typename TZ, bool S>
 hipError_t combine_bwd(const CombineBwdParams& p, hipStream_t s) {
   // a wave per token up to 1024 columns (two rounds of 512), a workgroup above
   const bool wave = p.cols <= 1024;
@@ -372,9 +384,9 @@ hipError_t combine_bwd(const CombineBwdParams& p, hipStream_t s) {
     const uint32_t all = wgs + (p.dz && t0 == 0 ? pad_wgs(p.total_rows) : 0);
     if (!all) return hipSuccess;
     if (wave)
-      ufp4_combine_bwd_kernel<TD, TZ, 64><<<all, kRowThreads, 0, s>>>(p, t0, wgs);
+      ufp4_combine_bwd_kernel<TD, TZ, 64, S><<<all, kRowThreads, 0, s>>>(p, t0, wgs);
     else
-      ufp4_combine_bwd_kernel<TD, TZ, kRowThreads><<<all, kRowThreads, 0, s>>>(p, t0, wgs);
+      ufp4_combine_bwd_kernel<TD, TZ, kRowThreads, S><<<all, kRowThreads, 0, s>>>(p, t0, wgs);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
@@ -399,23 +411,27 @@ hipError_t launch_expert_sort(const SortParams& p, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_expert_dispatch(const DispatchParams& p, hipStream_t s) {
-  if (p.x) return dispatch<-1>(p, s);
-  return p.format == kCkptINT8 ? dispatch<kCkptINT8>(p, s) : dispatch<kCkptE4M3>(p, s);
+namespace {
+
+template <bool S>
+hipError_t dispatch_from(const DispatchParams& p, hipStream_t s) {
+  if (p.x) return dispatch<-1, S>(p, s);
+  return p.format == kCkptINT8 ? dispatch<kCkptINT8, S>(p, s) : dispatch<kCkptE4M3, S>(p, s);
 }
 
-hipError_t launch_expert_combine(const CombineParams& p, hipStream_t s) {
+template <bool S>
+hipError_t combine(const CombineParams& p, hipStream_t s) {
   const int64_t lanes = (p.cols + 7) / 8, step = kMaxRowItems / lanes;
   for (int64_t t0 = 0; t0 < p.tokens; t0 += step) {
     const int64_t n = p.tokens - t0 < step ? p.tokens - t0 : step;
     const uint32_t items = (uint32_t)(n * lanes), wgs = (items + kRowThreads - 1) / kRowThreads;
     const FastDiv d = fast_div((uint32_t)lanes);
     if (p.z_f32) {
-      if (p.out_f32) ufp4_combine_kernel<float, float><<<wgs, kRowThreads, 0, s>>>(p, t0, items, d);
-      else ufp4_combine_kernel<float, uint16_t><<<wgs, kRowThreads, 0, s>>>(p, t0, items, d);
+      if (p.out_f32) ufp4_combine_kernel<float, float, S><<<wgs, kRowThreads, 0, s>>>(p, t0, items, d);
+      else ufp4_combine_kernel<float, uint16_t, S><<<wgs, kRowThreads, 0, s>>>(p, t0, items, d);
     } else {
-      if (p.out_f32) ufp4_combine_kernel<uint16_t, float><<<wgs, kRowThreads, 0, s>>>(p, t0, items, d);
-      else ufp4_combine_kernel<uint16_t, uint16_t><<<wgs, kRowThreads, 0, s>>>(p, t0, items, d);
+      if (p.out_f32) ufp4_combine_kernel<uint16_t, float, S><<<wgs, kRowThreads, 0, s>>>(p, t0, items, d);
+      else ufp4_combine_kernel<uint16_t, uint16_t, S><<<wgs, kRowThreads, 0, s>>>(p, t0, items, d);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -423,9 +439,27 @@ hipError_t launch_expert_combine(const CombineParams& p, hipStream_t s) {
   return hipSuccess;
 }
 
+template <bool S>
+hipError_t combine_backward(const CombineBwdParams& p, hipStream_t s) {
+  if (p.d_f32) return p.z_f32 ? combine_bwd<float, float, S>(p, s) : combine_bwd<float, uint16_t, S>(p, s);
+  return p.z_f32 ? combine_bwd<uint16_t, float, S>(p, s) : combine_bwd<uint16_t, uint16_t, S>(p, s);
+}
+
+}  // namespace
+
+hipError_t launch_expert_dispatch(const DispatchParams& p, hipStream_t s) {
+  return (p.tokens + p.total_rows) * p.cols * 2 > kLastLevelCache ? dispatch_from<true>(p, s) : dispatch_from<false>(p, s);
+}
+
+hipError_t launch_expert_combine(const CombineParams& p, hipStream_t s) {
+  const int64_t bytes = p.tokens * p.cols * (p.slots * (p.z_f32 ? 4 : 2) + (p.out_f32 ? 4 : 2));
+  return bytes > kLastLevelCache ? combine<true>(p, s) : combine<false>(p, s);
+}
+
 hipError_t launch_expert_combine_backward(const CombineBwdParams& p, hipStream_t s) {
-  if (p.d_f32) return p.z_f32 ? combine_bwd<float, float>(p, s) : combine_bwd<float, uint16_t>(p, s);
-  return p.z_f32 ? combine_bwd<uint16_t, float>(p, s) : combine_bwd<uint16_t, uint16_t>(p, s);
+  const int64_t rows = p.total_rows * ((p.dz ? 1 : 0) + (p.dw ? 1 : 0));
+  const int64_t bytes = p.cols * (rows * (p.z_f32 ? 4 : 2) + p.tokens * (p.d_f32 ? 4 : 2));
+  return bytes > kLastLevelCache ? combine_backward<true>(p, s) : combine_backward<false>(p, s);
 }
 
 }  // namespace ufp4

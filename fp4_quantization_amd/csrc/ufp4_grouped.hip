@@ -110,7 +110,7 @@ __device__ __forceinline__ RowTile find_tile(const GroupedParams& p, const Segme
 // Two neighbouring values of a row of C, n of them inside it.
 __device__ __forceinline__ void store_c(float* c, float v0, float v1, int n) {
   if (n >= 2)
-    store_8<4>(c, v32x2{__float_as_uint(v0), __float_as_uint(v1)});
+    store_8(c, v32x2{__float_as_uint(v0), __float_as_uint(v1)});
   else if (n == 1)
     *c = v0;
 }
@@ -442,7 +442,7 @@ __device__ __forceinline__ void store_c4(float* c, const f32x4& v, int n) {
 }
 __device__ __forceinline__ void store_c4(uint16_t* c, const f32x4& v, int n) {
   if (n >= 4) {
-    store_8<2>(c, v32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
+    store_8(c, v32x2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])});
   } else {
     store_c(c, v[0], v[1], n);
     store_c(c + 2, v[2], v[3], n - 2);

@@ -24,6 +24,8 @@ inline FastDiv fast_div(uint32_t d) {
   return f;
 }
 
+constexpr int64_t kLastLevelCache = (int64_t)256 << 20;  // bytes, MI355X
+
 constexpr int kMaxExperts = 1023;  // + the padding segment = the grouped quantizer's 1024
 constexpr int kMaxSlots = 1024;
 constexpr int kMaxAlign = 4096;

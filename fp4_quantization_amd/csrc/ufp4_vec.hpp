@@ -12,35 +12,36 @@ namespace ufp4 {
 typedef uint32_t v32x2 __attribute__((ext_vector_type(2)));
 typedef uint32_t v32x4 __attribute__((ext_vector_type(4)));
 
-// 16 and 8 bytes at an address aligned to A bytes.  gfx950 runs with
+// 16 and 8 bytes at any address.  gfx950 runs with
 // unaligned vector access to global memory on, so these are one instruction
 // at every alignment (an odd row width only costs the extra cache lines that
 // a vector straddles).
-template <int A>
-struct __attribute__((packed, aligned(A))) Bytes16 {
-  uint32_t w[4];
-};
-template <int A>
-struct __attribute__((packed, aligned(A))) Bytes8 {
-  uint32_t w[2];
-};
-template <int A>
+// S: past the caches (nontemporal), for calls whose data does not fit them.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(1)));
+typedef uint32_t u32x2_any __attribute__((ext_vector_type(2), aligned(1)));
+template <bool S = false>
 __device__ __forceinline__ v32x4 load16(const void* p) {
-  const Bytes16<A> b = *reinterpret_cast<const Bytes16<A>*>(p);
-  return v32x4{b.w[0], b.w[1], b.w[2], b.w[3]};
+  const u32x4_any* q = static_cast<const u32x4_any*>(p);
+  const u32x4_any v = S ? __builtin_nontemporal_load(q) : *q;
+  return v32x4{v.x, v.y, v.z, v.w};
 }
-template <int A>
+template <bool S = false>
 __device__ __forceinline__ void store_16(void* p, v32x4 v) {
-  *reinterpret_cast<Bytes16<A>*>(p) = Bytes16<A>{{v.x, v.y, v.z, v.w}};
+  u32x4_any* q = static_cast<u32x4_any*>(p);
+  if (S) __builtin_nontemporal_store(u32x4_any{v.x, v.y, v.z, v.w}, q);
+  else *q = u32x4_any{v.x, v.y, v.z, v.w};
 }
-template <int A>
+template <bool S = false>
 __device__ __forceinline__ v32x2 load8(const void* p) {
-  const Bytes8<A> b = *reinterpret_cast<const Bytes8<A>*>(p);
-  return v32x2{b.w[0], b.w[1]};
+  const u32x2_any* q = static_cast<const u32x2_any*>(p);
+  const u32x2_any v = S ? __builtin_nontemporal_load(q) : *q;
+  return v32x2{v.x, v.y};
 }
-template <int A>
+template <bool S = false>
 __device__ __forceinline__ void store_8(void* p, v32x2 v) {
-  *reinterpret_cast<Bytes8<A>*>(p) = Bytes8<A>{{v.x, v.y}};
+  u32x2_any* q = static_cast<u32x2_any*>(p);
+  if (S) __builtin_nontemporal_store(u32x2_any{v.x, v.y}, q);
+  else *q = u32x2_any{v.x, v.y};
 }
 
 // Two fp32 values to a bf16 pair (round to nearest even, NaN stays NaN).
@@ -64,17 +65,19 @@ __device__ __forceinline__ v32x4 pack(const V8& a) {
   return v32x4{pack_bf16(a.v[0], a.v[1]), pack_bf16(a.v[2], a.v[3]), pack_bf16(a.v[4], a.v[5]),
                pack_bf16(a.v[6], a.v[7])};
 }
+template <bool S = false>
 __device__ __forceinline__ V8 row_load(const uint16_t* p, int n) {
-  if (n >= 8) return unpack(load16<2>(p));
+  if (n >= 8) return unpack(load16<S>(p));
   V8 r;
 #pragma unroll
   for (int i = 0; i < 8; ++i) r.v[i] = i < n ? from_bf16(p[i]) : 0.0f;
   return r;
 }
+template <bool S = false>
 __device__ __forceinline__ V8 row_load(const float* p, int n) {
   V8 r;
   if (n >= 8) {
-    const v32x4 a = load16<4>(p), b = load16<4>(p + 4);
+    const v32x4 a = load16<S>(p), b = load16<S>(p + 4);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       r.v[i] = __uint_as_float(a[i]);
@@ -86,16 +89,18 @@ __device__ __forceinline__ V8 row_load(const float* p, int n) {
   for (int i = 0; i < 8; ++i) r.v[i] = i < n ? p[i] : 0.0f;
   return r;
 }
+template <bool S = false>
 __device__ __forceinline__ void row_store(uint16_t* p, const V8& a, int n) {
   const v32x4 w = pack(a);
   if (n >= 8) {
-    store_16<2>(p, w);
+    store_16<S>(p, w);
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
 }
+template <bool S = false>
 __device__ __forceinline__ void row_store(float* p, const V8& a, int n) {
   if (n >= 8) {
     v32x4 x, y;
@@ -104,8 +109,8 @@ __device__ __forceinline__ void row_store(float* p, const V8& a, int n) {
       x[i] = __float_as_uint(a.v[i]);
       y[i] = __float_as_uint(a.v[4 + i]);
     }
-    store_16<4>(p, x);
-    store_16<4>(p + 4, y);
+    store_16<S>(p, x);
+    store_16<S>(p + 4, y);
     return;
   }
 #pragma unroll
@@ -113,34 +118,38 @@ __device__ __forceinline__ void row_store(float* p, const V8& a, int n) {
     if (i < n) p[i] = a.v[i];
 }
 // Raw bf16 bits, moved without conversion.
+template <bool S = false>
 __device__ __forceinline__ v32x4 row_bits(const uint16_t* p, int n) {
-  if (n >= 8) return load16<2>(p);
+  if (n >= 8) return load16<S>(p);
   v32x4 r = {0u, 0u, 0u, 0u};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) r[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
   return r;
 }
+template <bool S = false>
 __device__ __forceinline__ void row_store_bits(uint16_t* p, v32x4 w, int n) {
   if (n >= 8) {
-    store_16<2>(p, w);
+    store_16<S>(p, w);
     return;
   }
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
 }
+template <bool S = false>
 __device__ __forceinline__ v32x2 code_bits(const uint8_t* p, int n) {
-  if (n >= 8) return load8<1>(p);
+  if (n >= 8) return load8<S>(p);
   v32x2 r = {0u, 0u};
 #pragma unroll
   for (int i = 0; i < 8; ++i)
     if (i < n) r[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
   return r;
 }
+template <bool S = false>
 __device__ __forceinline__ void code_store(uint8_t* p, v32x2 w, int n) {
   if (n >= 8) {
-    store_8<1>(p, w);
+    store_8<S>(p, w);
     return;
   }
 #pragma unroll
