@@ -189,6 +189,63 @@ __global__ __launch_bounds__(kSortThreads) void ufp4_sort_place_kernel(SortParam
 // rows, kPadRows a wave, and zero them.  Bound by the stores.
 constexpr int kRowThreads = 256, kPadRows = 16;
 
+// The rows of up to kSlotGroup slots from j0 on, read together (a slot past the
+// last one reads the last one's place); -1 where there is none.
+constexpr int kSlotGroup = 8;
+__device__ __forceinline__ void load_rows(const int32_t* rs, int j0, int slots, int64_t total_rows, int32_t (&r)[kSlotGroup]) {
+#pragma unroll
+  for (int j = 0; j < kSlotGroup; ++j) r[j] = rs[j0 + j < slots ? j0 + j : slots - 1];
+#pragma unroll
+  for (int j = 0; j < kSlotGroup; ++j) r[j] = j0 + j < slots && r[j] >= 0 && r[j] < total_rows ? r[j] : -1;
+}
+
+// Eight values of a row as loaded, so that the loads of several rows can be
+// under way together; those of no row count as zeros whatever row was read.
+struct Raw16 {
+  v32x4 w;
+};
+struct Raw32 {
+  v32x4 a, b;
+};
+template <bool S>
+__device__ __forceinline__ Raw16 raw_load(const uint16_t* p, int n) {
+  return Raw16{row_bits<S>(p, n)};
+}
+template <bool S>
+__device__ __forceinline__ Raw32 raw_load(const float* p, int n) {
+  const V8 v = row_load<S>(p, n);
+  Raw32 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    r.a[i] = __float_as_uint(v.v[i]);
+    r.b[i] = __float_as_uint(v.v[4 + i]);
+  }
+  return r;
+}
+__device__ __forceinline__ V8 raw_values(const Raw16& r, bool ok) {
+  const v32x4 none = {0u, 0u, 0u, 0u};
+  return unpack(ok ? r.w : none);
+}
+__device__ __forceinline__ V8 raw_values(const Raw32& r, bool ok) {
+  V8 v;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v.v[i] = ok ? __uint_as_float(r.a[i]) : 0.0f;
+    v.v[4 + i] = ok ? __uint_as_float(r.b[i]) : 0.0f;
+  }
+  return v;
+}
+template <typename T>
+struct RawOf;
+template <>
+struct RawOf<uint16_t> {
+  using type = Raw16;
+};
+template <>
+struct RawOf<float> {
+  using type = Raw32;
+};
+
 // Source of eight values: bf16 rows, or a checkpoint (FMT).
 template <int FMT>
 __device__ __forceinline__ v32x4 dispatch_load(const DispatchParams& p, int64_t t, int32_t col, int n) {
@@ -236,11 +293,17 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_dispatch_kernel(DispatchPara
   const int32_t col = (int32_t)(8 * (i - tt * lanes.d));
   const int64_t t = t0 + tt;
   const int n = p.cols - col < 8 ? (int)(p.cols - col) : 8;
-  const v32x4 w = dispatch_load<FMT>(p, t, col, n);
   const int32_t* rs = p.row_of_slot + t * p.slots;
-  for (int j = 0; j < p.slots; ++j) {
-    const int32_t r = rs[j];
-    if (r >= 0 && r < p.total_rows) row_store_bits<S>(p.out + (int64_t)r * p.ldo + col, w, n);
+  int32_t r[kSlotGroup];
+  load_rows(rs, 0, p.slots, p.total_rows, r);
+  const v32x4 w = dispatch_load<FMT>(p, t, col, n);
+  for (int j0 = 0;;) {
+#pragma unroll
+    for (int j = 0; j < kSlotGroup; ++j)
+      if (r[j] >= 0) row_store_bits<S>(p.out + (int64_t)r[j] * p.ldo + col, w, n);
+    j0 += kSlotGroup;
+    if (j0 >= p.slots) break;
+    load_rows(rs, j0, p.slots, p.total_rows, r);
   }
 }
 
@@ -258,27 +321,39 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_combine_kernel(CombineParams
   const int n = p.cols - col < 8 ? (int)(p.cols - col) : 8;
   const int32_t* rs = p.row_of_slot + t * p.slots;
   V8 acc{};
-  for (int j = 0; j < p.slots; ++j) {
-    const int32_t r = rs[j];
-    if (r < 0 || r >= p.total_rows) continue;
-    const float w = p.weights ? p.weights[t * p.slots + j] : 1.0f;
-    const V8 z = row_load<S>(static_cast<const TZ*>(p.z) + (int64_t)r * p.ldz + col, n);
+  for (int j0 = 0; j0 < p.slots && p.total_rows > 0; j0 += kSlotGroup) {
+    int32_t r[kSlotGroup];
+    float w[kSlotGroup];
+    typename RawOf<TZ>::type z[kSlotGroup];
+    load_rows(rs, j0, p.slots, p.total_rows, r);
 #pragma unroll
-    for (int k = 0; k < 8; ++k) acc.v[k] = __builtin_fmaf(w, z.v[k], acc.v[k]);
+    for (int j = 0; j < kSlotGroup; ++j)
+      w[j] = p.weights ? p.weights[t * p.slots + (j0 + j < p.slots ? j0 + j : p.slots - 1)] : 1.0f;
+#pragma unroll
+    for (int j = 0; j < kSlotGroup; ++j)
+      if (j0 + j < p.slots)
+        z[j] = raw_load<S>(static_cast<const TZ*>(p.z) + (int64_t)(r[j] < 0 ? 0 : r[j]) * p.ldz + col, n);
+#pragma unroll
+    for (int j = 0; j < kSlotGroup; ++j)
+      if (j0 + j < p.slots) {
+        const V8 v = raw_values(z[j], r[j] >= 0);
+        const float f = r[j] >= 0 ? w[j] : 0.0f;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) acc.v[k] = __builtin_fmaf(f, v.v[k], acc.v[k]);
+      }
   }
   row_store<S>(static_cast<TO*>(p.out) + t * p.ldo + col, acc, n);
 }
 
 // ------------------------------------------------------ combine's gradient
 // THREADS threads (a wave or a workgroup) per token: eight columns of dout are
-// held while up to kBwdSlots slots take their products with z (fp32 partial
+// held while up to kSlotGroup slots take their products with z (fp32 partial
 // sums a lane, summed over lanes in a fixed order) and their rows of dz.
-constexpr int kBwdSlots = 8;
 
 template <typename TD, typename TZ, int THREADS, bool S>
 __global__ __launch_bounds__(kRowThreads) void ufp4_combine_bwd_kernel(CombineBwdParams p, int64_t t0,
                                                                        uint32_t item_wgs) {
-  __shared__ float part[kRowThreads / 64][kBwdSlots];
+  __shared__ float part[kRowThreads / 64][kSlotGroup];
   if (blockIdx.x >= item_wgs) {
     const int64_t w = (int64_t)(blockIdx.x - item_wgs) * (kRowThreads / 64) + (threadIdx.x >> 6);
     zero_padding(p.slot_of_row, p.tokens * p.slots, w * kPadRows, p.total_rows, static_cast<TZ*>(p.dz), p.lddz,
@@ -288,30 +363,39 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_combine_bwd_kernel(CombineBw
   const int lane = threadIdx.x & (THREADS - 1);
   const int64_t t = t0 + (int64_t)blockIdx.x * (kRowThreads / THREADS) + threadIdx.x / THREADS;
   const bool live = t < p.tokens;  // (every thread reaches the barriers)
-  for (int j0 = 0; j0 < p.slots; j0 += kBwdSlots) {
-    int32_t row[kBwdSlots];
-    float w[kBwdSlots], dot[kBwdSlots];
+  for (int j0 = 0; j0 < p.slots; j0 += kSlotGroup) {
+    int32_t row[kSlotGroup];
+    float w[kSlotGroup], dot[kSlotGroup];
+    const int64_t tt = live ? t : 0;
+    load_rows(p.row_of_slot + tt * p.slots, j0, p.slots, p.total_rows, row);
 #pragma unroll
-    for (int j = 0; j < kBwdSlots; ++j) {
-      const bool in = live && j0 + j < p.slots;
-      const int32_t r = in ? p.row_of_slot[t * p.slots + j0 + j] : -1;
-      row[j] = r < p.total_rows ? r : -1;
-      w[j] = in && p.weights ? p.weights[t * p.slots + j0 + j] : 1.0f;
+    for (int j = 0; j < kSlotGroup; ++j) {
+      w[j] = p.weights ? p.weights[tt * p.slots + (j0 + j < p.slots ? j0 + j : p.slots - 1)] : 1.0f;
       dot[j] = 0.0f;
     }
     if (live)
       for (int64_t col = 8 * lane; col < p.cols; col += 8 * THREADS) {
         const int n = p.cols - col < 8 ? (int)(p.cols - col) : 8;
+        typename RawOf<TZ>::type z[kSlotGroup];
         const V8 d = row_load(static_cast<const TD*>(p.d) + t * p.ldd + col, n);
+        if (p.dw && p.total_rows > 0) {
 #pragma unroll
-        for (int j = 0; j < kBwdSlots; ++j) {
-          if (row[j] < 0) continue;
-          if (p.dw) {
-            const V8 z = row_load<S>(static_cast<const TZ*>(p.z) + (int64_t)row[j] * p.ldz + col, n);
+          for (int j = 0; j < kSlotGroup; ++j)
+            if (j0 + j < p.slots)
+              z[j] = raw_load<S>(static_cast<const TZ*>(p.z) + (int64_t)(row[j] < 0 ? 0 : row[j]) * p.ldz + col, n);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) dot[j] = __builtin_fmaf(d.v[k], z.v[k], dot[j]);
-          }
-          if (p.dz) {
+          for (int j = 0; j < kSlotGroup; ++j)
+            if (j0 + j < p.slots) {
+              const V8 v = raw_values(z[j], row[j] >= 0);
+              // (a dropped slot's sum stays 0 whatever dout holds)
+#pragma unroll
+              for (int k = 0; k < 8; ++k) dot[j] = row[j] >= 0 ? __builtin_fmaf(d.v[k], v.v[k], dot[j]) : 0.0f;
+            }
+        }
+        if (p.dz) {
+#pragma unroll
+          for (int j = 0; j < kSlotGroup; ++j) {
+            if (row[j] < 0) continue;
             V8 o;
 #pragma unroll
             for (int k = 0; k < 8; ++k) o.v[k] = w[j] * d.v[k];
@@ -321,20 +405,20 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_combine_bwd_kernel(CombineBw
       }
     if (!p.dw) continue;
 #pragma unroll
-    for (int j = 0; j < kBwdSlots; ++j)
+    for (int j = 0; j < kSlotGroup; ++j)
 #pragma unroll
       for (int m = 32; m >= 1; m >>= 1) dot[j] += __shfl_xor(dot[j], m);
     if (THREADS == 64) {
 #pragma unroll
-      for (int j = 0; j < kBwdSlots; ++j)
+      for (int j = 0; j < kSlotGroup; ++j)
         if (live && lane == j && j0 + j < p.slots) p.dw[t * p.slots + j0 + j] = dot[j];
     } else {
       __syncthreads();
 #pragma unroll
-      for (int j = 0; j < kBwdSlots; ++j)
+      for (int j = 0; j < kSlotGroup; ++j)
         if ((threadIdx.x & 63) == j) part[threadIdx.x >> 6][j] = dot[j];
       __syncthreads();
-      if (live && lane < kBwdSlots && j0 + lane < p.slots) {
+      if (live && lane < kSlotGroup && j0 + lane < p.slots) {
         float s = 0.0f;
         for (int q = 0; q < kRowThreads / 64; ++q) s += part[q][lane];
         p.dw[t * p.slots + j0 + lane] = s;
