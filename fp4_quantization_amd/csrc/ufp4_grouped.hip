@@ -285,13 +285,8 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
   // ---- consumers.  At the barrier that ends a producers' step the step's
   // buffer is complete and the other one is free again.
   const int wm = (wave >> 1) * 64, wn = (wave & 1) * 128;
-  int fa_at[kTileK / 16], fb_at[kTileK / 16];
-#pragma unroll
-  for (int kk = 0; kk < kTileK / 16; ++kk) {
-    const int at = lds_at(lane & 31, 2 * kk + (lane >> 5));
-    fa_at[kk] = at + wm * kLineHalves;
-    fb_at[kk] = at + wn * kLineHalves;
-  }
+  // chunk 2 kk + h of a line is chunk h with bits 1 and 2 of its place flipped
+  const int a_at = lds_at(lane & 31, lane >> 5) + wm * kLineHalves, b_at = lds_at(lane & 31, lane >> 5) + wn * kLineHalves;
   for (uint32_t id = blockIdx.x; id < g.ids; id += gridDim.x) {
     const Tile T = tile_at<DW>(p, S, id, g);
     if (T.e < 0) continue;
@@ -307,20 +302,30 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
       for (int h = 0; h < 2; ++h) {
         __syncthreads();
         if (!busy) continue;
+        // Fragments are requested ahead of their use: A's of the next 16 values
+        // during this ones', B's two before their turn (two matrix
+        // instructions each, and as many of the SIMD's other consumer between).
+        f16x8 fa[2][2], fb[3];
+        auto read_a = [&](int kk, int i) {
+          fa[kk & 1][i] = *reinterpret_cast<const f16x8*>(As[h] + (a_at ^ (16 * kk)) + 32 * i * kLineHalves);
+        };
+        auto read_b = [&](int n) {  // n: column tile n % 4 of values 16 (n / 4) ..
+          fb[n % 3] = *reinterpret_cast<const f16x8*>(Bs[h] + (b_at ^ (16 * (n >> 2))) + 32 * (n & 3) * kLineHalves);
+        };
+        read_a(0, 0);
+        read_b(0);
+        read_a(0, 1);
+        read_b(1);
 #pragma unroll
-        for (int kk = 0; kk < kTileK / 16; ++kk) {
-          f16x8 fa[2], fb[4];
+        for (int n = 0; n < 16; ++n) {
+          const int kk = n >> 2, j = n & 3;
+          if (n + 2 < 16) read_b(n + 2);
+          if (kk < 3 && (j == 1 || j == 2)) read_a(kk + 1, j - 1);
+          __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
           for (int i = 0; i < 2; ++i)
-            fa[i] = *reinterpret_cast<const f16x8*>(As[h] + fa_at[kk] + 32 * i * kLineHalves);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            fb[j] = *reinterpret_cast<const f16x8*>(Bs[h] + fb_at[kk] + 32 * j * kLineHalves);
-#pragma unroll
-          for (int i = 0; i < 2; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fa[kk & 1][i], fb[n % 3], acc[i][j], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
         }
       }
     }
