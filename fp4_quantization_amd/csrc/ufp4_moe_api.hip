@@ -10,7 +10,7 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 25;
 constexpr int64_t kMaxRows = (int64_t)1 << 28;  // a launch covers four threads a row
-constexpr int64_t kMaxTiles = 0xFFFF;             // 256-line tiles on a grid's second axis
+constexpr int64_t kMaxLines = (int64_t)0xFFFF * 256;  // of a grouped product's matrices
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 bool type_ok(int32_t t) { return t == UFP4_BF16 || t == UFP4_F32; }
@@ -234,9 +234,9 @@ int ufp4_checkpoint_load(const uint8_t* codes, const uint16_t* scales, int64_t r
 
 int ufp4_gated_act(const uint16_t* gu, int64_t rows, int64_t width, int64_t ld, int32_t act, uint16_t* h, int64_t ldh,
                    int32_t format, uint8_t* codes, uint16_t* scales, ufp4_stream_t stream) {
-  if (rows < 0 || width < 0 || ld < 2 * width || ldh < width || act < 0 || act > 1 || !format_ok(format))
-    return UFP4_ERR_INVALID_ARGUMENT;
-  if (2 * width >= kMaxDim || rows >= kMaxRows) return UFP4_ERR_SHAPE;
+  if (rows < 0 || width < 0 || act < 0 || act > 1 || !format_ok(format)) return UFP4_ERR_INVALID_ARGUMENT;
+  if (width >= kMaxDim / 2 || rows >= kMaxRows) return UFP4_ERR_SHAPE;
+  if (ld < 2 * width || ldh < width) return UFP4_ERR_INVALID_ARGUMENT;
   if (!codes != !scales) return UFP4_ERR_INVALID_ARGUMENT;
   if (rows == 0 || width == 0) return UFP4_OK;
   if (!gu || !h) return UFP4_ERR_INVALID_ARGUMENT;
@@ -258,10 +258,9 @@ int ufp4_gated_act(const uint16_t* gu, int64_t rows, int64_t width, int64_t ld, 
 int ufp4_gated_act_backward(const uint16_t* dh, int64_t lddh, const uint8_t* codes, const uint16_t* scales,
                             int32_t format, int64_t rows, int64_t width, int32_t act, uint16_t* dgu, int64_t lddg,
                             uint16_t* h_out, int64_t ldho, ufp4_stream_t stream) {
-  if (rows < 0 || width < 0 || lddh < width || lddg < 2 * width || (h_out && ldho < width) || act < 0 || act > 1 ||
-      !format_ok(format))
-    return UFP4_ERR_INVALID_ARGUMENT;
-  if (2 * width >= kMaxDim || rows >= kMaxRows) return UFP4_ERR_SHAPE;
+  if (rows < 0 || width < 0 || act < 0 || act > 1 || !format_ok(format)) return UFP4_ERR_INVALID_ARGUMENT;
+  if (width >= kMaxDim / 2 || rows >= kMaxRows) return UFP4_ERR_SHAPE;
+  if (lddh < width || lddg < 2 * width || (h_out && ldho < width)) return UFP4_ERR_INVALID_ARGUMENT;
   if (rows == 0 || width == 0) return UFP4_OK;
   if (!dh || !codes || !scales || !dgu) return UFP4_ERR_INVALID_ARGUMENT;
   if (!aligned(dh, 2) || !aligned(dgu, 2) || !aligned(h_out, 2) || !aligned(scales, 2)) return UFP4_ERR_ALIGNMENT;
@@ -289,7 +288,7 @@ int ufp4_gemm_grouped_nt(const ufp4_config* cfg, int64_t total_rows, int64_t N, 
   if (total_rows < 0 || N < 0 || K < 0 || ldc < N || num_groups < 1 || num_groups > 1024 || !type_ok(c_type) ||
       (b_layout != 0 && b_layout != 1))
     return UFP4_ERR_INVALID_ARGUMENT;
-  if (K % 32 || K >= kMaxDim || (b_layout == 1 && K * num_groups >= kMaxDim) || (N + 255) / 256 > kMaxTiles || total_rows >= kMaxDim) return UFP4_ERR_SHAPE;
+  if (K % 32 || K >= kMaxDim || (b_layout == 1 && K * num_groups >= kMaxDim) || N > kMaxLines || total_rows >= kMaxDim) return UFP4_ERR_SHAPE;
   if (total_rows == 0 || N == 0) return UFP4_OK;
   if (!c || !offsets_dev) return UFP4_ERR_INVALID_ARGUMENT;
   if ((rc = grouped_operand(a, 16, K == 0)) || (rc = grouped_operand(b, 16, K == 0))) return rc;
@@ -317,8 +316,7 @@ int ufp4_gemm_grouped_dw(const ufp4_config* cfg, int64_t M, int64_t N, int64_t p
   if (rc) return rc;
   if (M < 0 || N < 0 || padded_rows < 0 || num_groups < 1 || num_groups > 1024 || !type_ok(c_type))
     return UFP4_ERR_INVALID_ARGUMENT;
-  if (padded_rows % 16 || (M + 255) / 256 > kMaxTiles || (N + 255) / 256 > kMaxTiles || padded_rows >= kMaxDim)
-    return UFP4_ERR_SHAPE;
+  if (padded_rows % 16 || M > kMaxLines || N > kMaxLines || padded_rows >= kMaxDim) return UFP4_ERR_SHAPE;
   if (M == 0 || N == 0) return UFP4_OK;
   if (!c || !offsets_dev) return UFP4_ERR_INVALID_ARGUMENT;
   if ((rc = grouped_operand(a, 16, padded_rows == 0)) || (rc = grouped_operand(b, 16, padded_rows == 0))) return rc;

@@ -276,3 +276,28 @@ def test_refusals(env):
         F.ufp4_gated_act(x, 2, torch.zeros((4, 32), dtype=torch.bfloat16, device="cuda"))
     with pytest.raises(ValueError):
         F.Checkpoint(c.codes, c.scales[:, :1], INT8)
+
+
+@pytest.mark.parametrize("act,fmt", [(SILU, INT8), (GELU, E4M3)])
+def test_large_calls_equal_their_parts(env, act, fmt):
+    """Calls that move more than the last-level cache holds take other loads
+    and stores."""
+    torch, F = env
+    rows, width = 17011, 2003
+    assert rows * width * 8 > 256 << 20
+    g = torch.Generator(device="cuda").manual_seed(5)
+    gu = torch.randn(rows, 2 * width, device="cuda", generator=g).to(torch.bfloat16)
+    dh = torch.randn(rows, width, device="cuda", generator=g).to(torch.bfloat16)
+    c = F.alloc_checkpoint(rows, width, fmt, halves=2)
+    new = lambda r, w: torch.empty((r, w), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    h, again, dgu = new(rows, width), new(rows, width), new(rows, 2 * width)
+    F.ufp4_gated_act(gu, act, h, c)
+    F.ufp4_gated_act_backward(dh, c, act, dgu, again)
+    for r in range(0, rows, 3000):
+        n = min(3000, rows - r)
+        pc = F.alloc_checkpoint(n, width, fmt, halves=2)
+        ph, pa, pd = new(n, width), new(n, width), new(n, 2 * width)
+        F.ufp4_gated_act(gu[r:r + n], act, ph, pc)
+        F.ufp4_gated_act_backward(dh[r:r + n], pc, act, pd, pa)
+        assert torch.equal(ph, h[r:r + n]) and torch.equal(pa, again[r:r + n]) and torch.equal(pd, dgu[r:r + n])
+        assert torch.equal(pc.codes, c.codes[r:r + n]) and torch.equal(pc.scales, c.scales[r:r + n])

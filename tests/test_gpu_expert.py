@@ -306,3 +306,48 @@ def test_wrapper_refusals(env):
         F.ufp4_expert_combine(out, ros, torch.zeros((4, 2), dtype=torch.float64, device="cuda"), x)
     with pytest.raises(ValueError):
         F.ufp4_expert_combine_backward(x, None, ros, sor, None, None, torch.zeros((4, 2), device="cuda"))
+
+
+def test_large_calls(env):
+    """Calls that move more than the last-level cache holds take other loads
+    and stores: the same results as their parts, which do not."""
+    torch, F = env
+    rng = np.random.default_rng(12)
+    T, k, E, cols = 5000, 8, 24, 4104
+    ids = torch.from_numpy(rng.integers(-1, E, size=(T, k)).astype(np.int32)).cuda()
+    off, ros, sor = gpu_sort(env, ids, E, 16)
+    R = sor.numel()
+    g = torch.Generator(device="cuda").manual_seed(3)
+    x = torch.randn(T, cols, device="cuda", generator=g).to(torch.bfloat16)
+    w = torch.rand(T, k, device="cuda", generator=g)
+    want = torch.where((sor >= 0)[:, None], x[(sor.clamp(min=0) // k).long()], 0)
+    rows = torch.full((R, cols), 3.0, dtype=torch.bfloat16, device="cuda")
+    assert (T + R) * cols * 2 > 256 << 20
+    F.ufp4_expert_dispatch(x, ros, sor, rows)
+    assert torch.equal(rows, want)
+    c = F.alloc_checkpoint(T, cols, F.CKPT_E4M3)
+    F.ufp4_checkpoint_save(x, c)
+    kept = torch.empty_like(x)
+    F.ufp4_checkpoint_load(c, kept)
+    F.ufp4_expert_dispatch_checkpoint(c, ros, sor, rows)
+    assert torch.equal(rows, torch.where((sor >= 0)[:, None], kept[(sor.clamp(min=0) // k).long()], 0))
+    F.ufp4_expert_dispatch(x, ros, sor, rows)
+    for dtype in (torch.bfloat16, torch.float32):
+        z = rows.to(dtype) * 0.5
+        y, part = torch.empty((T, cols), dtype=dtype, device="cuda"), torch.empty((500, cols), dtype=dtype, device="cuda")
+        F.ufp4_expert_combine(z, ros, w, y)
+        for t in range(0, T, 500):
+            F.ufp4_expert_combine(z, ros[t:t + 500], w[t:t + 500], part)
+            assert torch.equal(part, y[t:t + 500])
+        dz, dw = torch.empty_like(z), torch.empty_like(w)
+        F.ufp4_expert_combine_backward(x, z, ros, sor, w, dz, dw)
+        # columns of dz on their own; dw against 64 bits
+        small = torch.empty((R, 600), dtype=dtype, device="cuda")
+        for col in (0, 1000, cols - 600):
+            F.ufp4_expert_combine_backward(x[:, col:col + 600], None, ros, sor, w, small, None)
+            assert torch.equal(small, dz[:, col:col + 600])
+        for t in range(0, T, 1000):
+            r = ros[t:t + 1000].long()
+            terms = x[t:t + 1000, None, :].double() * z[r.clamp(min=0)].double()
+            terms = torch.where((r >= 0)[..., None], terms, 0.0)
+            assert ((dw[t:t + 1000].double() - terms.sum(-1)).abs() <= cols * 2.0 ** -24 * terms.abs().sum(-1)).all()
