@@ -257,6 +257,7 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
+            if (i < kPieces / 2 && 64 * i >= T.m_end - T.m0) continue;  // lines of waves without rows
             const f16x2 ds = expand_scales<GRID>(v[i].s);
             const f16x2 d = h ? f16x2{ds.y, ds.y} : f16x2{ds.x, ds.x};
             uint32_t e[8];
