@@ -44,6 +44,40 @@ __device__ __forceinline__ void store_8(void* p, v32x2 v) {
   else *q = u32x2_any{v.x, v.y};
 }
 
+// Fewer than eight values of 2 (or 1) bytes each, as the 4, 2 and 1 of them that
+// n's bits name, packed to the front: a row's end costs up to three accesses.
+typedef uint32_t u32_any __attribute__((aligned(1)));
+typedef uint16_t u16_any __attribute__((aligned(1)));
+__device__ __forceinline__ v32x4 tail_load(const uint16_t* p, int n) {
+  v32x2 a = {0u, 0u};
+  uint32_t b = 0, c = 0;
+  if (n & 4) a = load8(p);
+  if (n & 2) b = *reinterpret_cast<const u32_any*>(p + (n & 4));
+  if (n & 1) c = p[n & 6];
+  const uint32_t bc = n & 2 ? b : c, cb = n & 2 ? c : 0u;  // what follows the four
+  return n & 4 ? v32x4{a.x, a.y, bc, cb} : v32x4{bc, cb, 0u, 0u};
+}
+__device__ __forceinline__ void tail_store(uint16_t* p, v32x4 w, int n) {
+  const uint32_t w0 = n & 4 ? w.z : w.x, w1 = n & 4 ? w.w : w.y;
+  if (n & 4) store_8(p, v32x2{w.x, w.y});
+  if (n & 2) *reinterpret_cast<u32_any*>(p + (n & 4)) = w0;
+  if (n & 1) p[n & 6] = (uint16_t)(n & 2 ? w1 : w0);
+}
+__device__ __forceinline__ v32x2 tail_load(const uint8_t* p, int n) {
+  uint32_t a = 0, b = 0, c = 0;
+  if (n & 4) a = *reinterpret_cast<const u32_any*>(p);
+  if (n & 2) b = *reinterpret_cast<const u16_any*>(p + (n & 4));
+  if (n & 1) c = p[n & 6];
+  const uint32_t bc = n & 2 ? b | (c << 16) : c;
+  return n & 4 ? v32x2{a, bc} : v32x2{bc, 0u};
+}
+__device__ __forceinline__ void tail_store(uint8_t* p, v32x2 w, int n) {
+  const uint32_t r = n & 4 ? w.y : w.x;
+  if (n & 4) *reinterpret_cast<u32_any*>(p) = w.x;
+  if (n & 2) *reinterpret_cast<u16_any*>(p + (n & 4)) = (uint16_t)r;
+  if (n & 1) p[n & 6] = (uint8_t)(n & 2 ? r >> 16 : r);
+}
+
 // Two fp32 values to a bf16 pair (round to nearest even, NaN stays NaN).
 typedef float f32x2v __attribute__((ext_vector_type(2)));
 typedef __bf16 bf16x2v __attribute__((ext_vector_type(2)));
@@ -68,10 +102,7 @@ __device__ __forceinline__ v32x4 pack(const V8& a) {
 template <bool S = false>
 __device__ __forceinline__ V8 row_load(const uint16_t* p, int n) {
   if (n >= 8) return unpack(load16<S>(p));
-  V8 r;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) r.v[i] = i < n ? from_bf16(p[i]) : 0.0f;
-  return r;
+  return unpack(tail_load(p, n));
 }
 template <bool S = false>
 __device__ __forceinline__ V8 row_load(const float* p, int n) {
@@ -96,9 +127,7 @@ __device__ __forceinline__ void row_store(uint16_t* p, const V8& a, int n) {
     store_16<S>(p, w);
     return;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  tail_store(p, w, n);
 }
 template <bool S = false>
 __device__ __forceinline__ void row_store(float* p, const V8& a, int n) {
@@ -121,11 +150,7 @@ __device__ __forceinline__ void row_store(float* p, const V8& a, int n) {
 template <bool S = false>
 __device__ __forceinline__ v32x4 row_bits(const uint16_t* p, int n) {
   if (n >= 8) return load16<S>(p);
-  v32x4 r = {0u, 0u, 0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) r[i >> 1] |= (uint32_t)p[i] << (16 * (i & 1));
-  return r;
+  return tail_load(p, n);
 }
 template <bool S = false>
 __device__ __forceinline__ void row_store_bits(uint16_t* p, v32x4 w, int n) {
@@ -133,18 +158,12 @@ __device__ __forceinline__ void row_store_bits(uint16_t* p, v32x4 w, int n) {
     store_16<S>(p, w);
     return;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) p[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+  tail_store(p, w, n);
 }
 template <bool S = false>
 __device__ __forceinline__ v32x2 code_bits(const uint8_t* p, int n) {
   if (n >= 8) return load8<S>(p);
-  v32x2 r = {0u, 0u};
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) r[i >> 2] |= (uint32_t)p[i] << (8 * (i & 3));
-  return r;
+  return tail_load(p, n);
 }
 template <bool S = false>
 __device__ __forceinline__ void code_store(uint8_t* p, v32x2 w, int n) {
@@ -152,9 +171,7 @@ __device__ __forceinline__ void code_store(uint8_t* p, v32x2 w, int n) {
     store_8<S>(p, w);
     return;
   }
-#pragma unroll
-  for (int i = 0; i < 8; ++i)
-    if (i < n) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+  tail_store(p, w, n);
 }
 
 // ------------------------------------------------------- 8-bit checkpoint

@@ -95,7 +95,7 @@ def test_every_quotient(env, fmt):
 
 
 @pytest.mark.parametrize("fmt", [INT8, E4M3])
-@pytest.mark.parametrize("cols", [1, 5, 8, 31, 32, 33, 40, 97, 1365, 4096])
+@pytest.mark.parametrize("cols", [1, 2, 3, 4, 5, 6, 7, 8, 31, 32, 33, 34, 36, 38, 40, 97, 1365, 4096])
 def test_shapes_and_strides(env, fmt, cols):
     torch, F = env
     rng = np.random.default_rng(cols)
@@ -174,7 +174,7 @@ def tolerance(v, size):
 
 
 @pytest.mark.parametrize("act", [SILU, GELU])
-@pytest.mark.parametrize("rows,width,pad", [(1, 1, 0), (5, 8, 0), (8, 2048, 0), (9, 33, 1), (33, 1365, 0), (6, 96, 3), (7, 250, 8)])
+@pytest.mark.parametrize("rows,width,pad", [(1, 1, 0), (5, 8, 0), (8, 2048, 0), (9, 33, 1), (4, 2, 0), (4, 3, 0), (4, 4, 1), (4, 6, 0), (5, 39, 0), (33, 1365, 0), (6, 96, 3), (7, 250, 8)])
 def test_gated(env, act, rows, width, pad):
     torch, F = env
     rng = np.random.default_rng(rows + width)

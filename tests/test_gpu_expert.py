@@ -114,7 +114,7 @@ def matrix(torch, rng, rows, cols, dtype, pad=0, shift=0):
     return t[shift:].view(rows, cols + pad)[:, :cols]
 
 
-COLS = [1, 7, 8, 9, 64, 515, 1024, 1025, 1365, 4096]
+COLS = [1, 2, 3, 4, 5, 6, 7, 8, 9, 10, 12, 14, 64, 515, 1024, 1025, 1365, 4096]
 
 
 @pytest.mark.parametrize("cols", COLS)
