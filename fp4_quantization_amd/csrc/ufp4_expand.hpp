@@ -87,10 +87,10 @@ __device__ __forceinline__ void store16(const uint32_t o[8], _Float16* dst) {
 template <int GRID>
 constexpr int kExpandShift = GRID == kGridE1M2 ? 8 : GRID == kGridINT4 ? 9 : 0;
 
-// The scales of two neighbouring blocks from their E4M3 bytes.
+// The scales of two neighbouring blocks from their E4M3 bytes (sign bits 0).
 template <int GRID>
 __device__ __forceinline__ f16x2 expand_scales(uint32_t two_bytes) {
-  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)(two_bytes & 0x7F7Fu), kExpandShift<GRID> ? 128.0f : 1.0f, false);
+  return __builtin_amdgcn_cvt_scalef32_pk_f16_fp8((int)two_bytes, kExpandShift<GRID> ? 128.0f : 1.0f, false);
 }
 
 template <int GRID>

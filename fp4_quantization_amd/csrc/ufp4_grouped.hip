@@ -192,25 +192,21 @@ struct Piece {
 };
 constexpr uint32_t kOutside = 0xFFFFFFF0u;  // an offset past every buffer
 
-// The pieces of 128 values at `chunk`, whole.  off: the lane's byte offset of
-// the line's first piece; the chunk's goes into the scalar offset.
-__device__ __forceinline__ Piece load_piece(const Lines& b, uint32_t off, int chunk) {
-  Piece q;
-  q.c = __builtin_bit_cast(g32x4, __builtin_amdgcn_raw_buffer_load_b128(b.codes, (int)off, 64 * chunk, 0));
-  q.s = __builtin_amdgcn_raw_buffer_load_b16(b.scales, (int)(off / 8), 8 * chunk, 0);
-  return q;
+// off, scale: byte offsets of the lane's codes and scales; `chunk` chunks of 128
+// values behind them go into the scalar offset.
+__device__ __forceinline__ void load_piece(const Lines& b, uint32_t off, uint32_t scale, int chunk, Piece& v) {
+  v.c = __builtin_bit_cast(g32x4, __builtin_amdgcn_raw_buffer_load_b128(b.codes, (int)off, 64 * chunk, 0));
+  v.s = __builtin_amdgcn_raw_buffer_load_b16(b.scales, (int)scale, 8 * chunk, 0);
 }
-// The same where the range ends inside the chunk, `left` values behind the
-// piece's first: blocks outside get the scale zero.
-__device__ __forceinline__ Piece load_tail(const Lines& b, uint32_t off, int chunk, int left) {
-  const uint32_t at = off + 64 * (uint32_t)chunk;
-  const uint32_t o0 = left >= 16 ? at : kOutside, o1 = left >= 32 ? at + 8 : kOutside;
-  const g32x2 lo = __builtin_bit_cast(g32x2, __builtin_amdgcn_raw_buffer_load_b64(b.codes, (int)o0, 0, 0));
-  const g32x2 hi = __builtin_bit_cast(g32x2, __builtin_amdgcn_raw_buffer_load_b64(b.codes, (int)o1, 0, 0));
-  const uint32_t s0 = __builtin_amdgcn_raw_buffer_load_b8(b.scales, (int)(left >= 16 ? at / 8 : kOutside), 0, 0);
-  const uint32_t s1 = __builtin_amdgcn_raw_buffer_load_b8(b.scales, (int)(left >= 32 ? at / 8 + 1 : kOutside), 0, 0);
-  return Piece{g32x4{lo.x, lo.y, hi.x, hi.y}, s0 | (s1 << 8)};
+// The first block of a line, and zeros; zeros where it is not `mine`.
+__device__ __forceinline__ void load_block(const Lines& b, uint32_t off, bool mine, Piece& v) {
+  const int at = (int)(mine ? off : kOutside), scale = (int)(mine ? off / 8 : kOutside);
+  const g32x2 lo = __builtin_bit_cast(g32x2, __builtin_amdgcn_raw_buffer_load_b64(b.codes, at, 0, 0));
+  const g32x2 hi = __builtin_bit_cast(g32x2, __builtin_amdgcn_raw_buffer_load_b64(b.codes, (int)kOutside, 0, 0));
+  v.c = g32x4{lo.x, lo.y, hi.x, hi.y};
+  v.s = __builtin_amdgcn_raw_buffer_load_b8(b.scales, scale, 0, 0);
 }
+constexpr uint32_t kScaleBits = 0x7F7Fu;  // of a piece's two scales
 
 template <int GRID, bool DW, typename TC>
 __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(GroupedParams p, TileGrid g) {
@@ -234,50 +230,86 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
       if (T.e < 0 || T.K <= 0) continue;
       const Lines A = lines_of(p.a, T.m0, T.m_end - T.m0, T.ka);
       const Lines B = lines_of(p.b, T.b_line + T.n0, p.N - T.n0, T.kb);
-      uint32_t off[kPieces];
+      uint32_t off[kPieces], soff[kPieces];
 #pragma unroll
       for (int i = 0; i < kPieces / 2; ++i) {
         off[i] = (uint32_t)(l0 + 64 * i) * (uint32_t)(p.a.pitch / 2) + 16 * q;
         off[i + kPieces / 2] = (uint32_t)(b_line_of(l0) + 64 * i) * (uint32_t)(p.b.pitch / 2) + 16 * q;
       }
-      const int chunks = (T.K + 127) / 128, whole = T.K / 128;
-      auto load = [&](Piece (&v)[kPieces], int chunk) {
-        const int c = uniform(chunk);
-        if (c < whole) {
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i) v[i] = load_piece(i < kPieces / 2 ? A : B, off[i], c);
-        } else if (c < chunks) {
-#pragma unroll
-          for (int i = 0; i < kPieces; ++i)
-            v[i] = load_tail(i < kPieces / 2 ? A : B, off[i], c, T.K - 128 * c - 32 * q);
-        }
-      };
-      auto expand = [&](const Piece (&v)[kPieces]) {
+      // Block h of every piece of v; after the second one load(i) follows.
+      auto expand = [&](Piece (&v)[kPieces], uint32_t mask, auto load) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
           for (int i = 0; i < kPieces; ++i) {
-            if (i < kPieces / 2 && 64 * i >= T.m_end - T.m0) continue;  // lines of waves without rows
-            const f16x2 ds = expand_scales<GRID>(v[i].s);
-            const f16x2 d = h ? f16x2{ds.y, ds.y} : f16x2{ds.x, ds.x};
-            uint32_t e[8];
-            expand8_shifted<GRID>(h ? v[i].c.z : v[i].c.x, d, e);
-            expand8_shifted<GRID>(h ? v[i].c.w : v[i].c.y, d, e + 4);
-            _Float16* to = (i < kPieces / 2 ? As : Bs)[h] + 64 * (i % (kPieces / 2)) * kLineHalves;
-            *reinterpret_cast<g32x4*>(to + at0) = g32x4{e[0], e[1], e[2], e[3]};
-            *reinterpret_cast<g32x4*>(to + at1) = g32x4{e[4], e[5], e[6], e[7]};
+            if (i >= kPieces / 2 || 64 * i < T.m_end - T.m0) {  // (not the lines of waves without rows)
+              const f16x2 ds = expand_scales<GRID>(v[i].s & mask);
+              const f16x2 d = h ? f16x2{ds.y, ds.y} : f16x2{ds.x, ds.x};
+              uint32_t e[8];
+              expand8_shifted<GRID>(h ? v[i].c.z : v[i].c.x, d, e);
+              expand8_shifted<GRID>(h ? v[i].c.w : v[i].c.y, d, e + 4);
+              _Float16* to = (i < kPieces / 2 ? As : Bs)[h] + 64 * (i % (kPieces / 2)) * kLineHalves;
+              *reinterpret_cast<g32x4*>(to + at0) = g32x4{e[0], e[1], e[2], e[3]};
+              *reinterpret_cast<g32x4*>(to + at1) = g32x4{e[4], e[5], e[6], e[7]};
+            }
+            if (h == 1) load(i);
           }
           __syncthreads();
         }
       };
+      if (T.K <= 16) {  // a single block
+        Piece v[kPieces];
+#pragma unroll
+        for (int i = 0; i < kPieces; ++i) load_block(i < kPieces / 2 ? A : B, off[i], q == 0, v[i]);
+        expand(v, kScaleBits & 0x00FFu, [](int) {});
+        continue;
+      }
+      // Chunks are requested two ahead of the one that is expanded: piece by
+      // piece into the registers that the expansion has just read, so that loads
+      // are issued between vector instructions and not in one burst (65536 rows,
+      // 64 segments, N = K = 4096, one after the other on one device: 1850 us in
+      // bursts, 1785 so; weight gradients 1150, 1122).  A wait for a piece counts
+      // the loads behind it, so every request takes the same loads without a
+      // branch; behind the last chunk that one is requested again.
+      // In a chunk that the range ends in, a piece of which one block is left is
+      // read one block earlier, so that no access crosses the buffer's end, one
+      // that is outside is read from the line's start, and the scales of blocks
+      // that do not count are masked.
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) soff[i] = off[i] / 8;
+      const int chunks = (T.K + 127) / 128, whole = T.K / 128, left = T.K - 128 * whole - 32 * q;
+      const uint32_t end_mask = left >= 32 ? kScaleBits : left >= 16 ? kScaleBits & 0xFF00u : 0;
+      int at = 0;
+      auto request = [&](int chunk) {
+        if (chunk < whole) {
+          at = uniform(chunk);
+        } else if (chunk < chunks) {
+          at = 0;
+          const int by = left >= 32 ? 64 * whole : left >= 16 ? 64 * whole - 8 : -16 * q;
+#pragma unroll
+          for (int i = 0; i < kPieces; ++i) off[i] += by, soff[i] += by / 8;
+        }
+      };
+      auto load = [&](Piece (&v)[kPieces], int i) { load_piece(i < kPieces / 2 ? A : B, off[i], soff[i], at, v[i]); };
+      auto step = [&](Piece (&v)[kPieces], int chunk) {
+        request(chunk + 2);
+        expand(v, chunk < whole ? kScaleBits : end_mask, [&](int i) {
+          __builtin_amdgcn_sched_barrier(0);
+          load(v, i);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      };
       Piece u[kPieces], v[kPieces];
-      load(u, 0);
+      request(0);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) load(u, i);
+      request(1);
+#pragma unroll
+      for (int i = 0; i < kPieces; ++i) load(v, i);
       for (int c = 0; c < chunks; c += 2) {
-        load(v, c + 1);
-        expand(u);
+        step(u, c);
         if (c + 1 >= chunks) break;
-        load(u, c + 2);
-        expand(v);
+        step(v, c + 1);
       }
     }
     __syncthreads();  // the consumers' last step
@@ -404,7 +436,7 @@ __device__ __forceinline__ Stretch load_stretch(const Lines& b, uint32_t off, in
 // Piece i (32 values) as four MFMA fragments.
 template <int GRID>
 __device__ __forceinline__ void expand_piece(const Stretch& v, int i, f16x8 (&f)[4]) {
-  const f16x2 ds = expand_scales<GRID>((i < 2 ? v.s.x : v.s.y) >> (16 * (i & 1)));
+  const f16x2 ds = expand_scales<GRID>(((i < 2 ? v.s.x : v.s.y) >> (16 * (i & 1))) & kScaleBits);
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     uint32_t e[4];

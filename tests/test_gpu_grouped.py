@@ -181,6 +181,37 @@ def test_dw_grids_and_types(env, grid, bf16):
     run_dw(env, [100, 0, 1000, 7], 264, 272, grid, bf16, grid)
 
 
+@pytest.mark.parametrize("counts", [[16], [16, 16], [48], [1, 40, 70, 100, 140, 10, 250, 16], [176, 16, 16, 48]],
+                         ids=["one block", "two of one", "three blocks", "odd blocks", "ends in one block"])
+@pytest.mark.parametrize("M,N", [(1, 1), (257, 1), (3, 514), (256, 257)])
+@pytest.mark.parametrize("grid", [E1M2, INT4])
+def test_dw_ranges_that_end_anywhere(env, counts, M, N, grid):
+    """No block behind a segment's last one, and none before its first one,
+    reaches its sums, whatever its scale is: a segment's neighbours get NaN
+    scales."""
+    torch, F, _ = env
+    run_dw(env, counts, M, N, grid, False, M + 7 * N + len(counts))
+    rng = np.random.default_rng(M + N)
+    E = len(counts)
+    off = np.concatenate([[0], np.cumsum(counts)]).astype(np.int64)
+    cols = F.ufp4_grouped_col_offsets(off, 16)
+    a, b = operand(rng, M, int(cols[-1]), grid), operand(rng, N, int(cols[-1]), grid)
+    one, offsets = np.ones(E, np.float32), torch.from_numpy(off).cuda()
+    av, bv = values(*a, grid), values(*b, grid)
+    c = torch.empty((E, M, N), device="cuda")
+    for odd in (0, 1):
+        sa, sb = a[1].copy(), b[1].copy()
+        for e in range(odd, E, 2):
+            sa[:, cols[e] // 16:cols[e + 1] // 16] = 0x7F
+            sb[:, cols[e] // 16:cols[e + 1] // 16] = 0x7F
+        F.ufp4_gemm_grouped_dw(F.config(grid=grid), dev(torch, F, a[0], sa, one), dev(torch, F, b[0], sb, one), offsets, c)
+        got = c.double().cpu().numpy()
+        for e in range(1 - odd, E, 2):
+            x, w = av[:, cols[e]:cols[e + 1]], bv[:, cols[e]:cols[e + 1]]
+            close(got[e], x @ w.T, np.abs(x) @ np.abs(w).T, x.shape[1], False)
+        assert all(np.isnan(got[e]).all() for e in range(odd, E, 2))
+
+
 def test_products_of_the_quantizers_own_outputs(env):
     """Forward and gradients from ufp4_quantize_grouped's layouts against the
     oracle's dequantized values."""
