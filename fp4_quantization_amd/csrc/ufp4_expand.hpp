@@ -77,15 +77,19 @@ __device__ __forceinline__ void store16(const uint32_t o[8], _Float16* dst) {
 
 // ------------------------------------------------------------------------
 // The grouped products' expansion: the same values times 2^-kExpandShift, in
-// fewer operations.  A sign-magnitude code needs no table if its magnitude m
-// becomes the top bits of an fp16 fraction under the exponents 0 and 1, where
-// fp16 is linear (m 2^-16 for m = 0..7); the sign goes to the sign bit, so two
-// bitwise operations make four high bytes.  The scale is applied as d 2^7 (at
-// most 57344).  For E1M2 the result is value d 2^-8, for INT4 value d 2^-9: a
-// multiple of 2^-18 of at most 11 bits, exact in fp16 (subnormals included,
-// which the MFMA takes as they are).  E2M1 codes have a hardware conversion.
+// fewer operations.  fp16 is linear under the exponents 0 and 1 (bits b are
+// b 2^-24 up to 2047), so a code needs no table if it becomes the bits of one;
+// the scale is applied as d 2^7 (at most 57344).
+//   E1M2: the magnitude goes to bits 8..10 (m 2^-16), the sign to the sign bit;
+//     two bitwise operations make four high bytes.  The result is value d 2^-8.
+//   INT4: value + 8 goes to bits 4..7 ((value + 8) 2^-20), and one fused
+//     operation multiplies and takes the 8 off: value d 2^-13.  (11 operations
+//     for eight codes; over signs and magnitudes it were 18.)
+//   E2M1 codes have a hardware conversion: value d.
+// Every result is a multiple of 2^-22 of at most 11 bits, exact in fp16
+// (subnormals included, which the MFMA takes as they are).
 template <int GRID>
-constexpr int kExpandShift = GRID == kGridE1M2 ? 8 : GRID == kGridINT4 ? 9 : 0;
+constexpr int kExpandShift = GRID == kGridE1M2 ? 8 : GRID == kGridINT4 ? 13 : 0;
 
 // The scales of two neighbouring blocks from their E4M3 bytes (sign bits 0).
 template <int GRID>
@@ -96,13 +100,24 @@ __device__ __forceinline__ f16x2 expand_scales(uint32_t two_bytes) {
 template <int GRID>
 __device__ __forceinline__ void expand8_shifted(uint32_t w, f16x2 d, uint32_t out[4]) {
   f16x2 v[4];
+  if (GRID == kGridINT4) {
+    const uint32_t he = ((w << 4) & 0xF0F0F0F0u) ^ 0x80808080u, ho = (w & 0xF0F0F0F0u) ^ 0x80808080u;
+    const _Float16 eight = (_Float16)(-1.0f / 131072.0f);  // -8 2^-20
+    const f16x2 off = d * f16x2{eight, eight};
+    v[0] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x0C040C00u));
+    v[1] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x0C050C01u));
+    v[2] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x0C060C02u));
+    v[3] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x0C070C03u));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) out[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_fma(v[i], d, off));
+    return;
+  }
   if (GRID == kGridE2M1 || GRID == kGridE2M1C) {
     v[0] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 0);
     v[1] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 1);
     v[2] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 2);
     v[3] = __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(w, 1.0f, 3);
   } else {
-    if (GRID == kGridINT4) w = signmag8(w);
     const uint32_t he = (w & 0x07070707u) | ((w << 4) & 0x80808080u);
     const uint32_t ho = ((w >> 4) & 0x07070707u) | (w & 0x80808080u);
     v[0] = __builtin_bit_cast(f16x2, __builtin_amdgcn_perm(ho, he, 0x040C000Cu));
