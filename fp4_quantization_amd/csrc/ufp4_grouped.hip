@@ -24,10 +24,11 @@ namespace {
 //
 // Measured there: 1740 us, 1.26 PFLOP/s, where the library's fp16 product of
 // 16384^3 reaches 1.45; weight gradients of 4096 x 2048 1083 us, 1.02, of which
-// the 2.1 GB of stores would take 310 alone.  A step takes about 2630 clocks at
-// 1.9 GHz: 2048 of matrix instructions, 2400 of a producer wave by itself (260
-// vector instructions, 16 stores to LDS, 8 loads), which is what bounds it, and
-// the power that the matrix units take: 9% fewer clocks a step gave 4% of time.
+// the 2.1 GB of stores would take 310 alone.  A step takes about 2700 clocks at
+// 1.9 GHz: 2048 are the matrix instructions', 2500 a producer wave's beside them
+// (2050 by itself: 260 vector instructions, 16 stores to LDS, 8 loads) and 260
+// the stores' drain and the barrier.  The producers bound it, and the power that
+// the matrix units take: 9% fewer clocks a step gave 4% of time.
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
 constexpr int kConsumers = 8, kProducers = 4;
 constexpr uint32_t kXcds = 8;
@@ -36,10 +37,10 @@ constexpr int kTileThreads = 64 * (kConsumers + kProducers);
 constexpr int kPieces = (kTileM + kTileN) / (16 * kProducers);  // per producer lane
 
 // LDS: [A, B][buffer][line][64 fp16] (both buffers of an operand inside the
-// 16-bit offset of an LDS instruction).  The eight 16-byte chunks of a line are stored in the order chunk ^ swizzle(line):
-// the same chunk of neighbouring lines (a fragment load) and neighbouring
-// chunks of a line (an expansion store of two lines) then fall on different
-// banks.
+// 16-bit offset of an LDS instruction).  The eight 16-byte chunks of a line are
+// stored in the order chunk ^ swizzle(line): the same chunk of neighbouring lines
+// (a fragment load) and neighbouring chunks of a line (an expansion store of two
+// lines) then fall on different banks.
 constexpr int kLineHalves = kTileK;
 __device__ __forceinline__ int swizzle(int line) { return ((line >> 1) & 7) ^ (line & 1); }
 __device__ __forceinline__ int lds_at(int line, int chunk) { return line * kLineHalves + 8 * (chunk ^ swizzle(line)); }
