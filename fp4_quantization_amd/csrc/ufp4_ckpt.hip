@@ -19,15 +19,17 @@ constexpr int64_t kMaxItems = (int64_t)1 << 30;
 // f(g) = g sigma and f'(g) = sigma + g sigma (1 - sigma) y'(g) for the two
 // gates, sigma = sigmoid(y): SiLU has y = g; tanh-GELU has
 // y = 2 sqrt(2/pi) (g + 0.044715 g^3), whose argument is clamped to +-16,
-// where sigma is 0 or 1 to the last bit, so that no intermediate overflows.
+// where sigma is 0 or 1 to the last bit, so that no intermediate overflows; a NaN
+// stays one (fminf and fmaxf would make it a bound).
 // The exponential and reciprocal are the hardware's (1 ulp), far inside the
 // bf16 rounding of every output.
 constexpr float kLog2e = 1.4426950408889634f;
+__device__ __forceinline__ float gelu_argument(float g) { return g < -16.0f ? -16.0f : (g > 16.0f ? 16.0f : g); }
 template <int ACT>
 __device__ __forceinline__ float gate_sigma(float g) {
   float y = g;
   if (ACT == 1) {
-    const float t = fminf(fmaxf(g, -16.0f), 16.0f);
+    const float t = gelu_argument(g);
     y = 1.5957691216057308f * t * __builtin_fmaf(0.044715f * t, t, 1.0f);
   }
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * y));
@@ -35,7 +37,7 @@ __device__ __forceinline__ float gate_sigma(float g) {
 template <int ACT>
 __device__ __forceinline__ float gate_slope(float g, float sg) {
   if (ACT == 0) return __builtin_fmaf(g * sg, 1.0f - sg, sg);
-  const float t = fminf(fmaxf(g, -16.0f), 16.0f);
+  const float t = gelu_argument(g);
   const float dy = 1.5957691216057308f * __builtin_fmaf(0.134145f * t, t, 1.0f);
   return __builtin_fmaf(t * dy * sg, 1.0f - sg, sg);
 }
