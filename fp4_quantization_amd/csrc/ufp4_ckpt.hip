@@ -21,8 +21,11 @@ constexpr int64_t kMaxItems = (int64_t)1 << 30;
 // y = 2 sqrt(2/pi) (g + 0.044715 g^3), whose argument is clamped to +-16,
 // where sigma is 0 or 1 to the last bit, so that no intermediate overflows; a NaN
 // stays one (fminf and fmaxf would make it a bound).
-// The exponential and reciprocal are the hardware's (1 ulp), far inside the
-// bf16 rounding of every output.
+// The exponential and reciprocal are the hardware's (1 ulp).  Below y = -80,
+// where exp(-y) nears its overflow and the reciprocal its subnormal results,
+// sigma is exp(y) itself, taken 2^64 too large (1 + exp(y) is 1 to the last bit).
+// So sigma is right to |y| 2^-23 relative, inside the bf16 rounding of every
+// output, down to fp32's subnormal numbers, and to their step of 2^-149 there.
 constexpr float kLog2e = 1.4426950408889634f;
 __device__ __forceinline__ float gelu_argument(float g) { return g < -16.0f ? -16.0f : (g > 16.0f ? 16.0f : g); }
 template <int ACT>
@@ -32,7 +35,9 @@ __device__ __forceinline__ float gate_sigma(float g) {
     const float t = gelu_argument(g);
     y = 1.5957691216057308f * t * __builtin_fmaf(0.044715f * t, t, 1.0f);
   }
-  return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * y));
+  const bool low = y < -80.0f;
+  const float e = __builtin_amdgcn_exp2f(low ? __builtin_fmaf(kLog2e, y, 64.0f) : -kLog2e * y);
+  return low ? e * 0x1p-64f : __builtin_amdgcn_rcpf(1.0f + e);
 }
 template <int ACT>
 __device__ __forceinline__ float gate_slope(float g, float sg) {
