@@ -525,8 +525,10 @@ def _lines(q: QTensor, lines: int, length: int, segments: int, name: str) -> Non
     if (tuple(q.codes.shape) != (lines, length // 2) or tuple(q.scales.shape) != (lines, length // 16)
             or not q.codes.is_contiguous() or not q.scales.is_contiguous()):
         raise ValueError(f"{name} must hold {lines} contiguous lines of {length} codes and their NV16 scales")
-    if q.tensor_scale.dtype != torch.float32 or q.tensor_scale.numel() < segments:
-        raise ValueError(f"{name} must have one float32 tensor scale a segment")
+    if q.codes.element_size() != 1 or q.scales.element_size() != 1:
+        raise ValueError(f"{name} must have codes and block scales of one byte")
+    if q.tensor_scale.dtype != torch.float32 or q.tensor_scale.numel() < segments or not q.tensor_scale.is_contiguous():
+        raise ValueError(f"{name} must have one float32 tensor scale a segment, side by side in memory")
 
 
 def ufp4_gemm_grouped_nt(cfg: ufp4_config, a: QTensor, b: QTensor, b_layout: int, offsets: torch.Tensor, K: int,
