@@ -50,8 +50,8 @@ def _record(stream, *objects) -> None:
 class ExpertLayer:
     """w_in: bf16 [experts, 2 hidden, width] (gate rows, then up rows); w_out:
     bf16 [experts, width, hidden]; width and hidden multiples of 32.  rht_seed
-    is shared by all operands; sr_seed keys the stochastic rounding of the
-    output gradients (give each step another one)."""
+    is shared by all operands; sr_seed, below 2^63, keys the stochastic rounding
+    of the output gradients (give each step and layer another one)."""
 
     def __init__(self, w_in: torch.Tensor, w_out: torch.Tensor, act: int = ACT_SILU, recipe: int = RECIPE_UFP4,
                  ckpt_format: int = CKPT_INT8, rht_seed: int = 0):
@@ -164,24 +164,29 @@ class ExpertLayer:
         dz, dweights = torch.empty_like(z), torch.empty_like(weights)
         ufp4_expert_combine_backward(dy, z, row_of_slot, slot_of_row, weights, dz, dweights)
 
-        def quantize(t, gemm, operand, rowwise):
-            return self._quantize(t, offsets, self._cfg(gemm, operand, sr_seed), rowwise, ws)
+        # dgu depends on the rounded dz, so it is rounded by other random numbers:
+        # by the same ones its mean would not be its value
+        key_dz, key_dgu = int(sr_seed), int(sr_seed) ^ (1 << 63)
 
-        def dw(dout, inp, M, N):
+        def quantize(t, gemm, operand, rowwise, key=0):
+            return self._quantize(t, offsets, self._cfg(gemm, operand, key), rowwise, ws)
+
+        def dw(dout, key, inp, M, N):
             c = torch.empty((E, M, N), dtype=torch.float32, device=dev)
-            ufp4_gemm_grouped_dw(self._cfg(GEMM_BWD_DW, OPERAND_A), quantize(dout, GEMM_BWD_DW, OPERAND_A, False),
+            ufp4_gemm_grouped_dw(self._cfg(GEMM_BWD_DW, OPERAND_A), quantize(dout, GEMM_BWD_DW, OPERAND_A, False, key),
                                  quantize(inp, GEMM_BWD_DW, OPERAND_B, False), offsets, c, E)
             return c
 
-        dh = self._nt(quantize(dz, GEMM_BWD_DX, OPERAND_A, True), self._w["out"][1], 1, offsets, W, F, GEMM_BWD_DX)
+        dh = self._nt(quantize(dz, GEMM_BWD_DX, OPERAND_A, True, key_dz), self._w["out"][1], 1, offsets, W, F, GEMM_BWD_DX)
         dgu = torch.empty((R, 2 * F), dtype=torch.bfloat16, device=dev)
         h = torch.empty((R, F), dtype=torch.bfloat16, device=dev)
         ufp4_gated_act_backward(dh, kept_gu, self.act, dgu, h)
-        dw_out = dw(dz, h, W, F)
+        dw_out = dw(dz, key_dz, h, W, F)
         rows = torch.empty((R, W), dtype=torch.bfloat16, device=dev)
         ufp4_expert_dispatch_checkpoint(kept_x, row_of_slot, slot_of_row, rows)
-        dw_in = dw(dgu, rows, 2 * F, W)
-        drows = self._nt(quantize(dgu, GEMM_BWD_DX, OPERAND_A, True), self._w["in"][1], 1, offsets, 2 * F, W, GEMM_BWD_DX)
+        dw_in = dw(dgu, key_dgu, rows, 2 * F, W)
+        drows = self._nt(quantize(dgu, GEMM_BWD_DX, OPERAND_A, True, key_dgu), self._w["in"][1], 1, offsets, 2 * F, W,
+                         GEMM_BWD_DX)
         dx = torch.empty((tokens, W), dtype=torch.bfloat16, device=dev)
         ufp4_expert_combine(drows, row_of_slot, None, dx)
         return dx, dw_in, dw_out, dweights
