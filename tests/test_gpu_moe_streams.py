@@ -78,3 +78,30 @@ def test_another_stream(env, one_stream):
     cur.wait_stream(s)
     for name, a, b in zip(("y", "dx", "dw_in", "dw_out", "dweights"), got, want):
         assert torch.equal(a, b), name
+
+
+def test_captured_in_a_graph(env):
+    """A forward and a backward pass captured once (on the capture's own
+    stream, the weights loaded on another) and replayed over changed inputs."""
+    torch, Layer = env
+    w_in, w_out, x, ids, w, dy = make(torch, 3)
+    layer = Layer(w_in, w_out, rht_seed=5)
+
+    def step():
+        y, saved = layer.forward(x, ids, w)
+        return (y, *layer.backward(saved, dy, sr_seed=7))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for seed in (8, 9, 10, 8):
+        for t, v in zip((x, ids, w, dy), make(torch, seed)[2:]):
+            t.copy_(v)
+        graph.replay()
+        copies = [t.clone() for t in got]
+        want = step()
+        torch.cuda.synchronize()
+        for name, a, b in zip(("y", "dx", "dw_in", "dw_out", "dweights"), copies, want):
+            assert torch.equal(a, b), name
