@@ -18,31 +18,39 @@ constexpr int64_t kMaxItems = (int64_t)1 << 30;
 
 // f(g) = g sigma and f'(g) = sigma + g sigma (1 - sigma) y'(g) for the two
 // gates, sigma = sigmoid(y): SiLU has y = g; tanh-GELU has
-// y = 2 sqrt(2/pi) (g + 0.044715 g^3), whose argument is clamped to +-16,
-// where sigma is 0 or 1 to the last bit, so that no intermediate overflows; a NaN
-// stays one (fminf and fmaxf would make it a bound).
+// y = 2 sqrt(2/pi) (g + 0.044715 g^3), infinite for large g, where sigma is 0 or 1.
 // The exponential and reciprocal are the hardware's (1 ulp).  Below y = -80,
 // where exp(-y) nears its overflow and the reciprocal its subnormal results,
-// sigma is exp(y) itself, taken 2^64 too large (1 + exp(y) is 1 to the last bit).
+// sigma is exp(y) itself, taken 2^64 too large (1 + exp(y) is 1 to the last bit);
+// few waves hold such a value, the others skip it (for every value: 4096 x 2048,
+// forward and backward, 28.9 us instead of 27.8 with GELU).
 // So sigma is right to |y| 2^-23 relative, inside the bf16 rounding of every
 // output, down to fp32's subnormal numbers, and to their step of 2^-149 there.
 constexpr float kLog2e = 1.4426950408889634f;
-__device__ __forceinline__ float gelu_argument(float g) { return g < -16.0f ? -16.0f : (g > 16.0f ? 16.0f : g); }
 template <int ACT>
-__device__ __forceinline__ float gate_sigma(float g) {
-  float y = g;
-  if (ACT == 1) {
-    const float t = gelu_argument(g);
-    y = 1.5957691216057308f * t * __builtin_fmaf(0.044715f * t, t, 1.0f);
+__device__ __forceinline__ V8 gate_sigma(const V8& g) {
+  V8 y, s;
+  float lowest = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const float t = g.v[k];
+    y.v[k] = ACT == 0 ? t : 1.5957691216057308f * t * __builtin_fmaf(0.044715f * t, t, 1.0f);
+    s.v[k] = __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(-kLog2e * y.v[k]));
+    lowest = fminf(lowest, y.v[k]);  // (passes over a NaN, whose sigma is NaN)
   }
-  const bool low = y < -80.0f;
-  const float e = __builtin_amdgcn_exp2f(low ? __builtin_fmaf(kLog2e, y, 64.0f) : -kLog2e * y);
-  return low ? e * 0x1p-64f : __builtin_amdgcn_rcpf(1.0f + e);
+  if (__any(lowest < -80.0f)) {
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+      if (y.v[k] < -80.0f) s.v[k] = __builtin_amdgcn_exp2f(__builtin_fmaf(kLog2e, y.v[k], 64.0f)) * 0x1p-64f;
+  }
+  return s;
 }
+// (GELU's y' is taken at a g clamped to +-16, beyond which sigma (1 - sigma) is 0
+// and y' must not be infinite; a NaN, which the clamp drops, is in sg)
 template <int ACT>
 __device__ __forceinline__ float gate_slope(float g, float sg) {
   if (ACT == 0) return __builtin_fmaf(g * sg, 1.0f - sg, sg);
-  const float t = gelu_argument(g);
+  const float t = fminf(fmaxf(g, -16.0f), 16.0f);
   const float dy = 1.5957691216057308f * __builtin_fmaf(0.134145f * t, t, 1.0f);
   return __builtin_fmaf(t * dy * sg, 1.0f - sg, sg);
 }
@@ -101,10 +109,10 @@ __global__ __launch_bounds__(kCkptThreads) void ufp4_gated_kernel(GatedParams p,
   const Item it = item_of(i, row0, lanes, (int32_t)p.width);
   const uint16_t* src = p.in + it.row * p.ld_in + it.col;
   const v32x4 gw = row_bits<S>(src, it.n), uw = row_bits<S>(src + p.width, it.n);
-  const V8 g = unpack(gw), u = unpack(uw);
+  const V8 g = unpack(gw), u = unpack(uw), sig = gate_sigma<ACT>(g);
   V8 h;
 #pragma unroll
-  for (int k = 0; k < 8; ++k) h.v[k] = g.v[k] * gate_sigma<ACT>(g.v[k]) * u.v[k];
+  for (int k = 0; k < 8; ++k) h.v[k] = g.v[k] * sig.v[k] * u.v[k];
   row_store<S>(p.h + it.row * p.ldh + it.col, h, it.n);
   if constexpr (FMT >= 0) {
     const uint32_t sg = ckpt_scale<FMT>(quad_max(bits_max(gw))), su = ckpt_scale<FMT>(quad_max(bits_max(uw)));
@@ -128,12 +136,12 @@ __global__ __launch_bounds__(kCkptThreads) void ufp4_gated_bwd_kernel(GatedParam
   const uint8_t* src = p.codes + it.row * 2 * p.width + it.col;
   const v32x2 gc = code_bits<S>(src, it.n), uc = code_bits<S>(src + p.width, it.n);
   const V8 dh = unpack(row_bits<S>(p.in + it.row * p.ld_in + it.col, it.n));
-  const V8 g = ckpt_decode<FMT>(gc, sg), u = ckpt_decode<FMT>(uc, su);
+  const V8 g = ckpt_decode<FMT>(gc, sg), u = ckpt_decode<FMT>(uc, su), sig = gate_sigma<ACT>(g);
   V8 dg, du, h;
 #pragma unroll
   for (int k = 0; k < 8; ++k) {
-    const float sig = gate_sigma<ACT>(g.v[k]), f = g.v[k] * sig;
-    dg.v[k] = dh.v[k] * u.v[k] * gate_slope<ACT>(g.v[k], sig);
+    const float f = g.v[k] * sig.v[k];
+    dg.v[k] = dh.v[k] * u.v[k] * gate_slope<ACT>(g.v[k], sig.v[k]);
     du.v[k] = dh.v[k] * f;
     h.v[k] = f * u.v[k];
   }
