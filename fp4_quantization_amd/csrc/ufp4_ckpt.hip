@@ -73,8 +73,8 @@ __device__ __forceinline__ Item item_of(uint32_t i, int64_t row0, const FastDiv&
   return it;
 }
 
-// 65536 x 4096: save 137 us, load 136, 6.0 TB/s; 8192 x 4096 17 us; 4099 x 1365,
-// odd alignment, 5.2 us, 3.3 TB/s.
+// 65536 x 4096: save 136 us, 6.1 TB/s, load 144, 5.7; 8192 x 4096 18 us; 4099 x
+// 1365, odd alignment, 6.0 us, 2.9 TB/s.
 template <int FMT>
 __global__ __launch_bounds__(kCkptThreads) void ufp4_ckpt_save_kernel(CkptParams p, int64_t row0, uint32_t items,
                                                                       FastDiv lanes) {
@@ -99,8 +99,8 @@ __global__ __launch_bounds__(kCkptThreads) void ufp4_ckpt_load_kernel(CkptParams
 }
 
 // FMT < 0: nothing is kept.  S: past the caches.  The exponentials and the codes
-// hide behind memory: 65536 x 2048 with an INT8 checkpoint 177 us for 1.09 GB,
-// 6.2 TB/s, its backward pass 217 us for 1.36 GB, 6.3 TB/s; 8 rows 2.5 us.
+// hide behind memory: 65536 x 2048 with an INT8 checkpoint 172 us for 1.09 GB,
+// 6.3 TB/s, its backward pass 225 us for 1.36 GB, 6.0 TB/s; 8 rows 2.8 us.
 template <int ACT, int FMT, bool S>
 __global__ __launch_bounds__(kCkptThreads) void ufp4_gated_kernel(GatedParams p, int64_t row0, uint32_t items,
                                                                   FastDiv lanes) {

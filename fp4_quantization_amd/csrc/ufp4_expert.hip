@@ -22,8 +22,9 @@ namespace {
 //     the waves' counts are summed in LDS.
 // Up to kSortSingle slots one workgroup does all three in one launch.  Bound by
 // the launches and, in the scan, by the one workgroup's latencies: 65536 slots,
-// 64 experts 2.4 + 7.4 + 4.0 us (counting with atomics on one array would save the
-// scan's loads but not fix the order); 64 slots 4.0 us in one launch.
+// 64 experts 4.8 + 7.7 + 4.9 us as profiled, 13 in a call (counting with atomics on
+// one array would save the scan's loads but not fix the order); 64 slots 4.0 us in one
+// launch.
 constexpr int kSortThreads = 1024, kSortWaves = kSortThreads / 64;
 constexpr int kSortBlocks = 64;
 constexpr int kSortSingle = 5120;  // (one launch 9.7 us at 4000 slots, 15.6 at 8192; three launches 12 to 13)
@@ -190,8 +191,12 @@ __global__ __launch_bounds__(kSortThreads) void ufp4_sort_place_kernel(SortParam
 // Each source row is read once and stored to the rows of its slots: an item is
 // eight columns of a token.  The workgroups past the tokens' look for padding
 // rows, kPadRows a wave, and zero them.  Bound by the stores: 8192 tokens of 4096
-// to 8 of 64 experts 107 us for 613 MB, 5.7 TB/s, where a copy reaches 4.7 and a
+// to 8 of 64 experts 111 us for 613 MB, 5.5 TB/s, where a copy reaches 4.7 and a
 // fill 6.8 (a workgroup per output row would read every token eight times).
+// Calls of one generation of waves are bound by a wave's own course instead, one
+// round of loads and then its stores: 3001 tokens of 1365 from an 8-bit checkpoint,
+// 4 slots, 8.6 waves a SIMD, 13.7 us for 40 MB (widths of whole 16 bytes 11.7),
+// where a fill of the output takes 7.0.
 constexpr int kRowThreads = 256, kPadRows = 16;
 
 // The rows of up to kSlotGroup slots from j0 on, read together (a slot past the
@@ -315,7 +320,7 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_dispatch_kernel(DispatchPara
 // --------------------------------------------------------------- combine
 // An item is eight columns of a token: the rows of its slots are read and
 // summed in slot order in fp32.  Bound by the loads of z: 8192 tokens of 4096, 8
-// slots, 100 us for 604 MB, 6.0 TB/s; 5119 of 2050, 6 slots, some dropped, 24 us.
+// slots, 95 us for 604 MB, 6.3 TB/s; 5119 of 2050, 6 slots, some dropped, 24 us.
 template <typename TZ, typename TO, bool S>
 __global__ __launch_bounds__(kRowThreads) void ufp4_combine_kernel(CombineParams p, int64_t t0, uint32_t items,
                                                                    FastDiv lanes) {
@@ -355,8 +360,8 @@ __global__ __launch_bounds__(kRowThreads) void ufp4_combine_kernel(CombineParams
 // THREADS threads (a wave or a workgroup) per token: eight columns of dout are
 // held while up to kSlotGroup slots take their products with z (fp32 partial
 // sums a lane, summed over lanes in a fixed order) and their rows of dz.  dout is
-// read once, z and dz once a slot: 8192 tokens of 4096, 8 slots, 218 us for 1.15
-// GB, 5.3 TB/s, bound by loads and stores.
+// read once, z and dz once a slot: 8192 tokens of 4096, 8 slots, 210 us for 1.15
+// GB, 5.5 TB/s, bound by loads and stores.
 template <typename TD, typename TZ, int THREADS, bool S>
 __global__ __launch_bounds__(kRowThreads) void ufp4_combine_bwd_kernel(CombineBwdParams p, int64_t t0,
                                                                        uint32_t item_wgs) {

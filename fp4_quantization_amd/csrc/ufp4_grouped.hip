@@ -22,13 +22,15 @@ namespace {
 // against 2548 where all waves expand and then multiply, both otherwise as they
 // were then).  All waves meet in one barrier per step.
 //
-// Measured there: 1740 us, 1.26 PFLOP/s, where the library's fp16 product of
-// 16384^3 reaches 1.45; weight gradients of 4096 x 2048 1083 us, 1.02, of which
-// the 2.1 GB of stores would take 310 alone.  A step takes about 2700 clocks at
-// 1.9 GHz: 2048 are the matrix instructions', 2500 a producer wave's beside them
-// (2050 by itself: 260 vector instructions, 16 stores to LDS, 8 loads) and 260
-// the stores' drain and the barrier.  The producers bound it, and the power that
-// the matrix units take: 9% fewer clocks a step gave 4% of time.
+// Measured there, medians of 20 calls in four runs: 1803 to 1823 us (single calls
+// 1726 to 2185), 1.21 PFLOP/s, where the library's fp16 product of 16384^3 reaches
+// 1.45; weight gradients of 4096 x 2048 1155 to 1159 us (1088 to 1278), 0.95, of
+// which the 2.1 GB of stores would take 310 alone.  A step takes 2640 clocks (3.07 M
+// clocks for a unit's 1160 steps), at 1.4 to 2.0 GHz from call to call: 2048 are the
+// matrix instructions', about 2500 a producer wave's beside them (2050 by itself: 260
+// vector instructions, 16 stores to LDS, 8 loads), the rest the stores' drain and
+// the barrier.  The producers bound it, and the power that the matrix units take:
+// 9% fewer clocks a step gave 4% of time.
 constexpr int kTileM = 256, kTileN = 256, kTileK = 64;
 constexpr int kConsumers = 8, kProducers = 4;
 constexpr uint32_t kXcds = 8;
@@ -412,7 +414,7 @@ __global__ __launch_bounds__(kTileThreads) void ufp4_grouped_tile_kernel(Grouped
 // 16-byte loads, its scales one of 8 bytes), the four lane groups of the MFMA
 // 512 of the line.  The MFMA's 32 values are then 8 of each group's, the same
 // ones of both operands, so nothing is exchanged between lanes.  128 rows, 64
-// segments, N = K = 4096: 108 us for 511 MB of codes and scales, 4.8 TB/s.
+// segments, N = K = 4096: 110 us for 511 MB of codes and scales, 4.6 TB/s.
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int kRowWaves = 4, kRowThreads = 64 * kRowWaves, kStretch = 512;
 
