@@ -76,7 +76,8 @@ enum ufp4_status {
 };
 
 /* Code layouts: E1M2, E2M1 and E2M1C store sign | magnitude index (index 0..7,
- * 0..7, 0..4); INT4 stores the two's-complement integer.  E2M1C is E2M1 with
+ * 0..7, 0..4); INT4 stores the two's-complement integer, -7..7 (the nibble 8 is
+ * not a code: no call writes it and no call defines its value).  E2M1C is E2M1 with
  * its range clamped to the uniformly spaced magnitudes {0, .5, 1, 1.5, 2}
  * (Qmax 2, MX32 element emax 1): the "simulated uniform" E2M1 alternative of
  * "Shrinkage Bias: The Hidden Geometric Trap in FP4 Training" (zhichai.net),
