@@ -16,7 +16,7 @@ from ._lib import (GEMM_BWD_DW, GEMM_BWD_DX, GEMM_FWD_Y, OPERAND_A, OPERAND_B, R
                    RECIPE_UFP4_INT4, TENSOR_DY, TENSOR_W, TENSOR_X,
                    GRID_E1M2, GRID_E2M1, GRID_E2M1C, GRID_INT4, LIB_PATH, ROUND_RTNE, ROUND_STOCHASTIC,
                    ACT_GELU_TANH, ACT_SILU, CKPT_E4M3, CKPT_INT8, TYPE_BF16, TYPE_F32,
-                   SCALE_MX32, SCALE_NV16, SCHEDULE_AUTO, SCHEDULE_SINGLE_PASS, SCHEDULE_TWO_PASS, Ufp4Error, check, lib, ufp4_config, ufp4_qtensor,
+                   SCALE_MX32, SCALE_NV16, SCHEDULE_AUTO, SCHEDULE_SINGLE_PASS, SCHEDULE_TWO_PASS, Ufp4Error, check, lib, ufp4_cache, ufp4_config, ufp4_qtensor,
                    ufp4_stats_t)
 
 __all__ = ["GRID_E1M2", "GRID_INT4", "GRID_E2M1", "GRID_E2M1C", "ROUND_RTNE", "ROUND_STOCHASTIC", "SCALE_NV16",
@@ -30,7 +30,8 @@ __all__ = ["GRID_E1M2", "GRID_INT4", "GRID_E2M1", "GRID_E2M1C", "ROUND_RTNE", "R
            "ACT_GELU_TANH", "Checkpoint", "alloc_checkpoint", "ufp4_expert_rows", "ufp4_expert_sort",
            "ufp4_expert_dispatch", "ufp4_expert_dispatch_checkpoint", "ufp4_expert_combine",
            "ufp4_expert_combine_backward", "ufp4_checkpoint_save", "ufp4_checkpoint_load", "ufp4_gated_act",
-           "ufp4_gated_act_backward", "ufp4_gemm_grouped_nt", "ufp4_gemm_grouped_dw"]
+           "ufp4_gated_act_backward", "ufp4_gemm_grouped_nt", "ufp4_gemm_grouped_dw", "ufp4_matvec", "MatvecWorkspace",
+           "QCache", "alloc_cache", "ufp4_cache_append", "ufp4_cache_read", "ufp4_tree_attention", "AttentionWorkspace"]
 
 
 def config(grid: int = GRID_E1M2, rounding: int = ROUND_RTNE, scaling: int = SCALE_NV16,
@@ -564,3 +565,207 @@ def ufp4_gemm_grouped_dw(cfg: ufp4_config, a: QTensor, b: QTensor, offsets: torc
     check("ufp4_gemm_grouped_dw",
           lib.ufp4_gemm_grouped_dw(ctypes.byref(cfg), M, N, P, a.c(), b.c(), _ptr(_int64(offsets, "offsets")), E,
                                    _ptr(c), kind, _stream(stream)))
+
+
+# ---------------------------------------------------------------- decoding
+
+class _on_device_of:
+    """The device that all of the tensors lie on, as the current one, and the
+    stream of a call there (None: the device's current stream)."""
+
+    def __init__(self, stream, *tensors):
+        index = -1
+        for t in tensors:
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError("every tensor of the call must lie on the GPU")
+            if index >= 0 and t.get_device() != index:
+                raise ValueError("all tensors of the call must lie on one device")
+            index = t.get_device()
+        if stream is not None and stream.device_index != index:
+            raise ValueError("the stream must belong to the device of the tensors")
+        self.index, self.stream = index, stream
+
+    def __enter__(self) -> int:
+        self.before = torch._C._cuda_getDevice()
+        if self.before != self.index:
+            torch._C._cuda_setDevice(self.index)
+        if self.stream is not None:
+            return self.stream.cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
+
+    def __exit__(self, *_):
+        if self.before != self.index:
+            torch._C._cuda_setDevice(self.before)
+
+
+class _Scratch:
+    """Device bytes of a call's workspace; nothing is kept in them between
+    calls, but calls that may run at the same time need one each."""
+
+    def __init__(self, nbytes: int, device):
+        self.nbytes = int(nbytes)
+        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
+
+    @property
+    def ptr(self):
+        return _ptr(self.buf)
+
+
+class MatvecWorkspace(_Scratch):
+    """Workspace of ufp4_matvec for up to `tokens` rows of x."""
+
+    def __init__(self, tokens: int, N: int, K: int, cfg: ufp4_config, device="cuda"):
+        super().__init__(lib.ufp4_matvec_workspace(ctypes.byref(cfg), int(tokens), int(N), int(K)), device)
+
+
+def ufp4_matvec(cfg: ufp4_config, x: torch.Tensor, w: QTensor, y: torch.Tensor, ws: MatvecWorkspace | None = None,
+                stream=None) -> None:
+    """y = x' times the quantized weight matrix transposed: x [tokens, K] and y
+    [tokens, N] bf16 or float32, w the row-wise layout of an N x K matrix under
+    cfg; x' is x, transformed as w was if cfg.rht.  ws may be None where
+    MatvecWorkspace(...).nbytes is 0."""
+    xt, tokens, K, ldx = _rows(x, "x")
+    yt, rows, N, ldy = _rows(y, "y")
+    block = block_len(cfg.scaling)
+    if rows != tokens:
+        raise ValueError("x and y must have one row a token")
+    if (tuple(w.codes.shape) != (N, K // 2) or tuple(w.scales.shape) != (N, K // block) or not w.codes.is_contiguous()
+            or not w.scales.is_contiguous() or w.codes.element_size() != 1 or w.scales.element_size() != 1):
+        raise ValueError(f"w must hold {N} contiguous lines of {K} codes and their scales, a byte each")
+    if w.tensor_scale.dtype != torch.float32 or w.tensor_scale.numel() < 1:
+        raise ValueError("w must have a float32 tensor scale")
+    with _on_device_of(stream, x, y, w.codes, w.scales, w.tensor_scale, ws.buf if ws else None) as s:
+        check("ufp4_matvec",
+              lib.ufp4_matvec(ctypes.byref(cfg), _ptr(x), xt, tokens, K, ldx, w.c(), N, _ptr(y), yt, ldy,
+                              ws.ptr if ws else None, ws.nbytes if ws else 0, s))
+
+
+class QCache:
+    """Device buffers of a 4-bit key-value cache (the layouts of ufp4_cache):
+    k_codes uint8 [pages, heads, page_tokens, dim / 2], k_scales [.., dim / 16],
+    v_codes uint8 [pages, heads, page_tokens / 32, dim / 2, 32], v_scales [..,
+    dim / 16, 32]; k_scale and v_scale float32 [heads] tensor scales, None: 1."""
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
+                 k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):
+        if k_codes.dim() != 4:
+            raise ValueError("k_codes must be [pages, heads, page_tokens, dim / 2]")
+        pages, heads, tokens, half = k_codes.shape
+        for t, shape in ((k_codes, (pages, heads, tokens, half)), (k_scales, (pages, heads, tokens, half // 8)),
+                         (v_codes, (pages, heads, tokens // 32, half, 32)),
+                         (v_scales, (pages, heads, tokens // 32, half // 8, 32))):
+            if tuple(t.shape) != shape or not t.is_contiguous() or t.element_size() != 1:
+                raise ValueError(f"codes and scales of the cache must be contiguous bytes of one geometry, here {shape}")
+        if tokens % 32 or half % 16:
+            raise ValueError("pages must hold a multiple of 32 tokens, heads a multiple of 32 values")
+        for t in (k_scale, v_scale):
+            if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (heads,) or not t.is_contiguous()):
+                raise ValueError("tensor scales must be contiguous float32 [heads]")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
+        self.k_scale, self.v_scale = k_scale, v_scale
+        self.pages, self.heads, self.page_tokens, self.dim = pages, heads, tokens, 2 * half
+        self.tensors = (k_codes, k_scales, v_codes, v_scales, k_scale, v_scale)
+
+    def c(self) -> ufp4_cache:
+        return ufp4_cache(*(_ptr(t) for t in self.tensors), self.pages, self.page_tokens, self.heads, self.dim)
+
+
+def alloc_cache(pages: int, page_tokens: int, heads: int, dim: int, k_scale: torch.Tensor | None = None,
+                v_scale: torch.Tensor | None = None, device="cuda") -> QCache:
+    """Buffers of an (unwritten) cache."""
+    def empty(*shape):
+        return torch.empty(shape, dtype=torch.uint8, device=device)
+
+    return QCache(empty(pages, heads, page_tokens, dim // 2), empty(pages, heads, page_tokens, dim // 16),
+                  empty(pages, heads, page_tokens // 32, dim // 2, 32),
+                  empty(pages, heads, page_tokens // 32, dim // 16, 32), k_scale, v_scale)
+
+
+def ufp4_cache_append(cfg: ufp4_config, cache: QCache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor,
+                      stream=None) -> None:
+    """Quantizes keys and values, bf16 [tokens, heads * dim], into the slots
+    (int64 [tokens]; page * page_tokens + place in the page; outside the cache:
+    dropped).  Slots must differ."""
+    rows, cols, ldk = _bf16_rows(k, "k")
+    vr, vcols, ldv = _bf16_rows(v, "v")
+    if (cols, vr, vcols) != (cache.heads * cache.dim, rows, cols) or slots.numel() != rows:
+        raise ValueError("k and v must be [tokens, heads * dim] with one slot a token")
+    with _on_device_of(stream, k, v, _int64(slots, "slots"), *cache.tensors) as s:
+        check("ufp4_cache_append",
+              lib.ufp4_cache_append(ctypes.byref(cfg), ctypes.byref(cache.c()), _ptr(k), ldk, _ptr(v), ldv, rows,
+                                    _ptr(slots), s))
+
+
+def ufp4_cache_read(cfg: ufp4_config, cache: QCache, slots: torch.Tensor, k_out: torch.Tensor | None,
+                    v_out: torch.Tensor | None, inverse_rht: bool = True, stream=None) -> None:
+    """The tokens at `slots` (int64 [tokens]; outside the cache: zeros) as k_out
+    and v_out [tokens, heads * dim], bf16 or float32 (either may be None);
+    inverse_rht: mapped back through the transform of cfg (pass False for a
+    cache written without it)."""
+    kinds, lds = [], []
+    for t, name in ((k_out, "k_out"), (v_out, "v_out")):
+        if t is None:
+            lds.append(0)
+            continue
+        kind, rows, cols, ld = _rows(t, name)
+        if (rows, cols) != (slots.numel(), cache.heads * cache.dim):
+            raise ValueError(f"{name} must be [tokens, heads * dim] with one row a slot")
+        kinds.append(kind)
+        lds.append(ld)
+    if len(set(kinds)) > 1:
+        raise TypeError("k_out and v_out must have one type")
+    with _on_device_of(stream, _int64(slots, "slots"), k_out, v_out, *cache.tensors) as s:
+        check("ufp4_cache_read",
+              lib.ufp4_cache_read(ctypes.byref(cfg), ctypes.byref(cache.c()), _ptr(slots), slots.numel(),
+                                  int(bool(inverse_rht)), _ptr(k_out), lds[0], _ptr(v_out), lds[1],
+                                  kinds[0] if kinds else TYPE_BF16, s))
+
+
+class AttentionWorkspace(_Scratch):
+    """Workspace of ufp4_tree_attention for up to `sequences` sequences of up to
+    max_draft drafted tokens, whatever their lengths."""
+
+    def __init__(self, cache: QCache, q_heads: int, sequences: int, max_draft: int, device=None):
+        n = lib.ufp4_tree_attention_workspace(ctypes.byref(cache.c()), int(q_heads), int(sequences), int(max_draft))
+        if n == 0:
+            raise ValueError("invalid attention shape")
+        super().__init__(n, cache.k_codes.device if device is None else device)
+
+
+def ufp4_tree_attention(cfg: ufp4_config, cache: QCache, q: torch.Tensor, q_offsets: torch.Tensor,
+                        lengths: torch.Tensor, page_table: torch.Tensor, max_draft: int, out: torch.Tensor,
+                        ws: AttentionWorkspace, mask: torch.Tensor | None = None, softmax_scale: float | None = None,
+                        lse: torch.Tensor | None = None, stream=None) -> None:
+    """Attention of each sequence's last tokens (one that is decoded, a chain, or
+    with `mask` a tree of drafted ones) over the cache that holds them.
+    q and out: bf16 [rows, q_heads * dim]; q_offsets int64 [sequences + 1], the
+    rows of each sequence (at most max_draft); lengths int32 [sequences], its
+    tokens in the cache, drafted ones included; page_table int32 [sequences,
+    pages a sequence]; mask int64 [rows], bit j: the row sees drafted token j of
+    its sequence (None: those up to itself); lse float32 [rows, q_heads];
+    softmax_scale defaults to dim ** -0.5."""
+    rows, width, ldq = _bf16_rows(q, "q")
+    orows, owidth, ldo = _bf16_rows(out, "out")
+    heads, rest = divmod(width, cache.dim)
+    if rest or heads < 1 or heads % cache.heads or (orows, owidth) != (rows, width):
+        raise ValueError("q and out must be [rows, q_heads * dim], q_heads a multiple of the cache's heads")
+    sequences = lengths.numel()
+    if q_offsets.numel() != sequences + 1:
+        raise ValueError("q_offsets must have one entry more than lengths")
+    if page_table.dim() != 2 or page_table.shape[0] != sequences:
+        raise ValueError("page_table must have one line a sequence")
+    if mask is not None and mask.numel() != rows:
+        raise ValueError("mask must have one entry a row of q")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (rows, heads) or not lse.is_contiguous()):
+        raise TypeError("lse must be a contiguous float32 tensor [rows, q_heads]")
+    scale = cache.dim ** -0.5 if softmax_scale is None else float(softmax_scale)
+    with _on_device_of(stream, q, out, _int64(q_offsets, "q_offsets"), _int32(lengths, "lengths"),
+                       _int32(page_table, "page_table"), None if mask is None else _int64(mask, "mask"), lse, ws.buf,
+                       *cache.tensors) as s:
+        check("ufp4_tree_attention",
+              lib.ufp4_tree_attention(ctypes.byref(cfg), ctypes.byref(cache.c()), _ptr(q), ldq, heads, _ptr(q_offsets),
+                                      sequences, rows, int(max_draft), _ptr(lengths), _ptr(page_table),
+                                      page_table.shape[1], _ptr(mask), scale, _ptr(out), ldo, _ptr(lse), ws.ptr,
+                                      ws.nbytes, s))

@@ -38,7 +38,9 @@ EXPORTED = ["ufp4_status_string", "ufp4_workspace_size", "ufp4_workspace_init",
             "ufp4_quantize_grouped_delayed", "ufp4_roof_rowcol",
             "ufp4_expert_rows", "ufp4_expert_sort", "ufp4_expert_dispatch", "ufp4_expert_dispatch_checkpoint",
             "ufp4_expert_combine", "ufp4_expert_combine_backward", "ufp4_checkpoint_save", "ufp4_checkpoint_load",
-            "ufp4_gated_act", "ufp4_gated_act_backward", "ufp4_gemm_grouped_nt", "ufp4_gemm_grouped_dw"]
+            "ufp4_gated_act", "ufp4_gated_act_backward", "ufp4_gemm_grouped_nt", "ufp4_gemm_grouped_dw",
+            "ufp4_matvec", "ufp4_matvec_workspace", "ufp4_cache_append", "ufp4_cache_read", "ufp4_tree_attention",
+            "ufp4_tree_attention_workspace"]
 
 
 class Ufp4Error(RuntimeError):
@@ -56,6 +58,13 @@ class ufp4_config(ctypes.Structure):
 class ufp4_qtensor(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
                 ("tensor_scale", ctypes.c_void_p)]
+
+
+class ufp4_cache(ctypes.Structure):
+    _fields_ = [("k_codes", ctypes.c_void_p), ("k_scales", ctypes.c_void_p), ("v_codes", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("k_tensor_scale", ctypes.c_void_p), ("v_tensor_scale", ctypes.c_void_p),
+                ("pages", ctypes.c_int64), ("page_tokens", ctypes.c_int32), ("heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32)]
 
 
 class ufp4_stats_t(ctypes.Structure):
@@ -129,7 +138,16 @@ def _load():
     L.ufp4_schedule_of.argtypes = [i64, i64, i32, i32, cfgp, ctypes.POINTER(i32)]
     L.ufp4_expert_rows.restype = i64
     L.ufp4_expert_rows.argtypes = [i64, i32, i32, i32]
+    cachep, f32 = ctypes.POINTER(ufp4_cache), ctypes.c_float
+    L.ufp4_matvec_workspace.restype = sz
+    L.ufp4_matvec_workspace.argtypes = [cfgp, i64, i64, i64]
+    L.ufp4_tree_attention_workspace.restype = sz
+    L.ufp4_tree_attention_workspace.argtypes = [cachep, i32, i32, i32]
     for name, args in (
+            ("ufp4_matvec", [cfgp, P, i32, i64, i64, i64, ufp4_qtensor, i64, P, i32, i64, P, sz, P]),
+            ("ufp4_cache_append", [cfgp, cachep, P, i64, P, i64, i64, P, P]),
+            ("ufp4_cache_read", [cfgp, cachep, P, i64, i32, P, i64, P, i64, i32, P]),
+            ("ufp4_tree_attention", [cfgp, cachep, P, i64, i32, P, i32, i64, i32, P, P, i64, P, f32, P, i64, P, P, sz, P]),
             ("ufp4_expert_sort", [P, i64, i32, i64, i32, i32, i64, P, P, P, P]),
             ("ufp4_expert_dispatch", [P, i64, i64, i64, i32, P, P, i64, P, i64, P]),
             ("ufp4_expert_dispatch_checkpoint", [P, P, i32, i64, i64, i32, P, P, i64, P, i64, P]),

@@ -10,7 +10,8 @@ from concurrent.futures import ThreadPoolExecutor
 _HERE = os.path.dirname(os.path.abspath(__file__))
 SOURCES = [os.path.join(_HERE, "csrc", f)
            for f in ("ufp4_quant.hip", "ufp4_misc.hip", "ufp4_gemm.hip", "ufp4_host.hip", "ufp4_api.hip",
-                     "ufp4_expert.hip", "ufp4_ckpt.hip", "ufp4_grouped.hip", "ufp4_moe_api.hip")]
+                     "ufp4_expert.hip", "ufp4_ckpt.hip", "ufp4_grouped.hip", "ufp4_moe_api.hip",
+                     "ufp4_matvec.hip", "ufp4_cache.hip", "ufp4_attend.hip", "ufp4_serve_api.hip")]
 OUT = os.path.join(_HERE, "libufp4.so")
 
 # -ffp-contract=off: no implicit fused multiply-add (every rounding step is

@@ -478,6 +478,131 @@ int ufp4_gemm_grouped_dw(const ufp4_config* cfg, int64_t M, int64_t N, int64_t p
                          ufp4_qtensor b, const int64_t* offsets_dev, int32_t num_groups, void* c, int32_t c_type,
                          ufp4_stream_t stream);
 
+/* --- decoding: few rows, a 4-bit cache, attention over it ---------------------- */
+
+/* Running a model on the formats above, token by token: products of a few
+ * tokens' rows with 4-bit weights, a key-value cache kept in 4 bits, and
+ * attention over it.  The quantization is that of ufp4_quantize (the formats,
+ * the transform and its reach: "Shrinkage Bias: The Hidden Geometric Trap in
+ * FP4 Training" (zhichai.net), "Key points"); applying it to a cache is a choice
+ * of this library, not of the pages. */
+
+/* y[t][n] = S * sum over k of x'[t][k] * w[n][k], t < tokens, n < N, for a
+ * weight matrix quantized row-wise (codes [N][K/2], scales [N][K/16] or
+ * [N][K/32], one tensor scale S; MX32: S is 1 and not read).  x' is x, or with
+ * cfg->rht != 0 the transform of x's 16-blocks under cfg->rht_seed (weights
+ * quantized with the same seed then give the product of the untransformed
+ * matrices).  x [tokens][ldx] and y [tokens][ldy] of x_type and y_type (enum
+ * ufp4_type), at any alignment of their elements.
+ * The weights enter exactly, and sums are fp32.  x' enters
+ *   NV16: as a sum of fp16 numbers under a power of two for each token, its
+ *     largest |x| in [2^14, 2^15) (with the transform, [2^12, 2^13)): one for
+ *     bf16 y, two (22 bits) for fp32 y.  A bf16 x without the transform is exact
+ *     in one down to 2^-28 of the token's largest.
+ *   MX32: as a sum of bf16 numbers: one, exact, for bf16 x without the
+ *     transform, else three (24 bits).  Weights and products below 2^-126 may
+ *     count as zero.
+ * Meant for few tokens: the weights are read once for every 64 of them.
+ * cfg: grid, scaling, rht, rht_seed.  K % 32 == 0, K and N below 2^25, tokens
+ * below 2^21 (UFP4_ERR_SHAPE); codes 16-byte and NV16 scales 2-byte aligned.  tokens or N
+ * of 0 writes nothing, K of 0 writes zeros.
+ * ws: ufp4_matvec_workspace bytes, 16-byte aligned (it may be 0: then ws may be
+ * NULL).  It needs no preparation and holds nothing between calls.  y must not
+ * overlap any other buffer of the call. */
+int ufp4_matvec(const ufp4_config* cfg, const void* x, int32_t x_type, int64_t tokens, int64_t K, int64_t ldx,
+                ufp4_qtensor w, int64_t N, void* y, int32_t y_type, int64_t ldy, void* ws, size_t ws_bytes,
+                ufp4_stream_t stream);
+
+/* Bytes of workspace ufp4_matvec needs; 0 also for arguments it refuses. */
+size_t ufp4_matvec_workspace(const ufp4_config* cfg, int64_t tokens, int64_t N, int64_t K);
+
+/* Keys and values of `heads` heads of `dim` values each, kept in 4 bits a value
+ * and an E4M3 scale for 16, in `pages` pages of page_tokens tokens.  Slot
+ * p * page_tokens + i is token i of page p.
+ *   keys:   k_codes [page][head][token][dim/2], k_scales [page][head][token][dim/16];
+ *   values: a page is page_tokens / 32 tiles of 32 tokens, and in a tile the
+ *     tokens of one pair of neighbouring values lie side by side:
+ *     v_codes [page][head][tile][dim/2][32], v_scales [page][head][tile][dim/16][32].
+ *   k_tensor_scale, v_tensor_scale: one float a head, the NV16 tensor scale S_t
+ *     = max / (Qmax * 448) for some largest magnitude max of the head's
+ *     (transformed) keys or values; larger blocks saturate.  NULL, or an entry
+ *     that is not a positive finite number: 1.
+ * dim a multiple of 32, at most 256; page_tokens a multiple of 32, at most 65536
+ * (UFP4_ERR_SHAPE); pages >= 0, pages * page_tokens below 2^40; heads in [1,
+ * 1024]; code and scale arrays 16-byte aligned.  The arrays need no preparation:
+ * what a slot holds before it is written is never read as a number. */
+typedef struct {
+  uint8_t* k_codes;
+  uint8_t* k_scales;
+  uint8_t* v_codes;
+  uint8_t* v_scales;
+  const float* k_tensor_scale;
+  const float* v_tensor_scale;
+  int64_t pages;
+  int32_t page_tokens, heads, dim;
+} ufp4_cache;
+
+/* Quantizes tokens' keys and values into their slots: k, v [tokens][ldk, ldv >=
+ * heads * dim] (bf16, any 2-byte alignment), slots int64 [tokens] on the device.
+ * Each block of 16 along a head becomes what ufp4_quantize would make of it
+ * under the head's S_t, rounded to nearest even.  A slot outside [0, pages *
+ * page_tokens) drops its token.  Slots of one call that are written must
+ * differ (what a slot named twice holds afterwards is not defined).
+ * cfg: NV16 and RTNE only (UFP4_ERR_INVALID_ARGUMENT); grid, rht, rht_seed. */
+int ufp4_cache_append(const ufp4_config* cfg, const ufp4_cache* cache, const uint16_t* k, int64_t ldk,
+                      const uint16_t* v, int64_t ldv, int64_t tokens, const int64_t* slots, ufp4_stream_t stream);
+
+/* The tokens at `slots` read back: k_out, v_out [tokens][ldk, ldv >= heads *
+ * dim] of out_type, value(code) * d_b and, with inverse_rht != 0, mapped back
+ * through the inverse transform, as ufp4_dequantize.  A slot outside the cache
+ * gives zeros; a slot may be named any number of times.  Either output may be
+ * NULL. */
+int ufp4_cache_read(const ufp4_config* cfg, const ufp4_cache* cache, const int64_t* slots, int64_t tokens,
+                    int32_t inverse_rht, void* k_out, int64_t ldk, void* v_out, int64_t ldv, int32_t out_type,
+                    ufp4_stream_t stream);
+
+/* Attention of each sequence's last tokens over the cache: the token that is
+ * being decoded, a chain, or a tree of drafted tokens, whose keys and values
+ * have been appended.  Sequence b has lengths[b] tokens in the cache; token j is
+ * in slot page_table[b][j / page_tokens] * page_tokens + j % page_tokens.  Its
+ * last n = q_offsets[b+1] - q_offsets[b] tokens are the drafted ones, with the
+ * rows q_offsets[b].. of q, out, lse and mask.  Drafted token i (row q_offsets[b]
+ * + i) sees token j < lengths[b] if
+ *   j < lengths[b] - n (the history), or
+ *   mask NULL: j <= lengths[b] - n + i (a chain: causal), or
+ *   mask: bit j - (lengths[b] - n) of mask[row] is set.
+ *   out[row][h] = sum over seen j of p_j v_j,  p = softmax of softmax_scale *
+ *     <q[row][h], k_j> over them, k and v of head h / (q_heads / heads);
+ *   lse[row][h] = ln of the sum of exp(softmax_scale <q, k_j>) (may be NULL).
+ * A row that sees nothing gets zeros, lse -infinity.
+ * q [q_rows][ldq] and out [q_rows][ldo], bf16, head h at columns h * dim; any
+ * 2-byte alignment; lse fp32 [q_rows][q_heads], dense; q_heads a multiple of
+ * heads.  With cfg->rht the cache holds transformed keys and values: q is
+ * transformed and out transformed back.
+ *   q_offsets: int64 [sequences + 1].  A sequence whose rows are not all inside
+ *     [0, q_rows) is left out; its rows, rows of no sequence, and drafted tokens
+ *     from max_draft on (a sequence has at most max_draft) are neither read nor
+ *     written.  max_draft <= 64 with a mask.
+ *   lengths: int32 [sequences], taken as if inside [0, ld_pages * page_tokens].
+ *   page_table: int32 [sequences][ld_pages]; the tokens of a page that is
+ *     outside [0, pages) are seen by no row.
+ * Logits are exact products in fp32 sums (transformed q in 22 bits), the softmax
+ * fp32; its weights enter the second product as fp16.
+ * cfg: NV16 only; grid, rht, rht_seed.  softmax_scale finite.  1 <= q_heads <=
+ * 8192, 1 <= max_draft, sequences <= 65535, q_rows < 2^28,
+ * ld_pages * page_tokens <= 2^30 (UFP4_ERR_INVALID_ARGUMENT,
+ * UFP4_ERR_SHAPE).  ws: ufp4_tree_attention_workspace bytes, 16-byte aligned; needs
+ * no preparation and holds nothing between calls. */
+int ufp4_tree_attention(const ufp4_config* cfg, const ufp4_cache* cache, const uint16_t* q, int64_t ldq,
+                        int32_t q_heads, const int64_t* q_offsets, int32_t sequences, int64_t q_rows,
+                        int32_t max_draft, const int32_t* lengths, const int32_t* page_table, int64_t ld_pages,
+                        const uint64_t* mask, float softmax_scale, uint16_t* out, int64_t ldo, float* lse, void* ws,
+                        size_t ws_bytes, ufp4_stream_t stream);
+
+/* Bytes of workspace ufp4_tree_attention needs for any lengths; 0 for arguments
+ * it refuses. */
+size_t ufp4_tree_attention_workspace(const ufp4_cache* cache, int32_t q_heads, int32_t sequences, int32_t max_draft);
+
 /* --- schedule ------------------------------------------------------------ */
 
 /* Dense NV16 calls need the tensor maximum before any code is written.

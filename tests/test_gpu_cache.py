@@ -1,0 +1,134 @@
+"""The 4-bit key-value cache: appended tokens against the oracle's quantizer,
+bit for bit, and what is read back."""
+import numpy as np
+import pytest
+import serve_reference as ref
+
+pytestmark = pytest.mark.gpu
+
+E1M2, INT4, E2M1, E2M1C = range(4)
+
+
+@pytest.fixture(scope="module")
+def env(orc):
+    torch = pytest.importorskip("torch")
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import fp4_quantization_amd as F
+    return torch, F, orc
+
+
+def bits(t):
+    import torch
+    return t.contiguous().view(torch.int16).cpu().numpy().view(np.uint16)
+
+
+def tensor_scales(torch, heads, grid, seed):
+    """(maxima, S_t) of each head: S_t = fl(max / fl(Qmax * 448))."""
+    g = np.random.default_rng(seed)
+    amax = (1.0 + 5.0 * g.random(heads)).astype(np.float32)
+    return amax, torch.from_numpy(amax / np.float32(ref.QMAX[grid] * 448.0)).cuda()
+
+
+def make(env, pages, P, H, D, grid, scaled=True, fill=0xA7):
+    torch, F, _ = env
+    ka, ks = tensor_scales(torch, H, grid, 1)
+    va, vs = tensor_scales(torch, H, grid, 2)
+    if not scaled:  # S_t = 1: what a largest magnitude of Qmax * 448 gives
+        ka = va = np.full(H, ref.QMAX[grid] * 448.0, np.float32)
+        ks = vs = None
+    c = F.alloc_cache(pages, P, H, D, ks, vs)
+    for t in c.tensors[:4]:
+        t.fill_(fill)
+    return c, ka, va
+
+
+def inputs(torch, T, width, seed, special):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    x = torch.randn(T, width, device="cuda", generator=g)
+    x *= torch.exp(2.0 * torch.randn(T, width // 16, device="cuda", generator=g)).repeat_interleave(16, 1)
+    if special:
+        f = x.view(-1)
+        i = torch.randperm(f.numel(), device="cuda", generator=g)[: max(1, f.numel() // 50)]
+        odd = torch.tensor([float("nan"), float("inf"), -float("inf"), 3e38, 1e-40, -0.0], device="cuda")
+        f[i] = odd[torch.arange(i.numel(), device="cuda") % 6]
+        x[0, :32] = 0.0
+    return x.to(torch.bfloat16)
+
+
+def check_written(env, cfg, c, k, v, slots, ka, va, fill=0xA7):
+    """Every slot's codes and scales are the oracle's, every other slot's are untouched."""
+    torch, F, orc = env
+    H, D, P = c.heads, c.dim, c.page_tokens
+    ocfg = orc.config(grid=cfg.grid, rht=cfg.rht, rht_seed=cfg.rht_seed)
+    want = [np.full(t.shape, fill, np.uint8) for t in c.tensors[:4]]
+    s = slots.cpu().numpy()
+    live = np.nonzero((s >= 0) & (s < c.pages * P))[0]
+    page, at = s[live] // P, s[live] % P
+    for h in range(H):
+        for x, amax, codes, scales, value in ((k, ka, want[0], want[1], False), (v, va, want[2], want[3], True)):
+            oc, os, _, _ = orc.quantize_given_amax(bits(x[:, h * D:(h + 1) * D]), ocfg, 0, float(amax[h]))
+            if value:
+                codes[page, h, at // 32, :, at % 32] = oc[live]
+                scales[page, h, at // 32, :, at % 32] = os[live]
+            else:
+                codes[page, h, at] = oc[live]
+                scales[page, h, at] = os[live]
+    for t, w in zip(c.tensors[:4], want):
+        assert np.array_equal(t.cpu().numpy(), w)
+
+
+CASES = [
+    # T, pages, P, H, D, grid, rht, scaled, special
+    (1, 2, 32, 1, 32, E1M2, 1, False, False), (1, 3, 64, 8, 128, E1M2, 1, True, False),
+    (5, 2, 32, 3, 96, INT4, 1, True, True), (33, 4, 96, 2, 64, E2M1, 0, True, True),
+    (200, 7, 64, 2, 160, E1M2, 0, True, True), (130, 3, 256, 5, 256, E2M1C, 1, False, False),
+    (1000, 40, 32, 1, 192, INT4, 0, False, True), (64, 5, 32, 2, 224, E2M1, 1, True, False),
+]
+
+
+@pytest.mark.parametrize("order", ["run", "scattered"])
+@pytest.mark.parametrize("T,pages,P,H,D,grid,rht,scaled,special", CASES)
+def test_append_and_read(env, T, pages, P, H, D, grid, rht, scaled, special, order):
+    torch, F, orc = env
+    cfg = F.config(grid=grid, rht=rht, rht_seed=9)
+    c, ka, va = make(env, pages, P, H, D, grid, scaled)
+    n = min(T, pages * P - 1)
+    if order == "run":  # neighbouring slots from the middle of a tile on
+        slots = (torch.arange(T, device="cuda") + min(5, pages * P - n)).long()
+    else:
+        slots = torch.randperm(pages * P, device="cuda", generator=torch.Generator(device="cuda").manual_seed(T)).long()
+        slots = slots[torch.arange(T, device="cuda") % slots.numel()]
+    # dropped tokens: before the cache, behind it, far out
+    slots[n:] = pages * P
+    for i, s in ((0, -1), (3, pages * P), (4, 1 << 62), (7, -(1 << 62))):
+        if T > 8:
+            slots[i] = s
+    # rows inside a wider buffer, at odd addresses
+    k = inputs(torch, T, H * D + 32, 3, special)[:, 1:1 + H * D]
+    v = inputs(torch, T, H * D + 16, 4, special)[:, 5:5 + H * D]
+    F.ufp4_cache_append(cfg, c, k, v, slots)
+    check_written(env, cfg, c, k, v, slots, ka, va)
+    # read back: the oracle's values in fp32, rounded once in bf16
+    live = (slots >= 0) & (slots < pages * P)
+    ocfg = orc.config(grid=grid, rht=rht, rht_seed=9)
+    want = []
+    for x, amax in ((k, ka), (v, va)):
+        w = np.zeros((T, H * D), np.float32)
+        for h in range(H):
+            oc, os, ts, _ = orc.quantize_given_amax(bits(x[:, h * D:(h + 1) * D]), ocfg, 0, float(amax[h]))
+            w[:, h * D:(h + 1) * D] = orc.dequantize(oc, os, ts, T, D, ocfg, bool(rht))
+        w[~live.cpu().numpy()] = 0.0
+        want.append(torch.from_numpy(w).cuda())
+    for kind in (torch.float32, torch.bfloat16):
+        full = [torch.full((T, H * D + 3), -7.0, dtype=kind, device="cuda") for _ in range(2)]
+        outs = [f[:, 2:2 + H * D] for f in full]
+        F.ufp4_cache_read(cfg, c, slots, *outs, bool(rht))
+        for o, w, f in zip(outs, want, full):
+            assert torch.equal(o, w.to(kind))
+            assert bool((f[:, :2] == -7.0).all()) and bool((f[:, 2 + H * D:] == -7.0).all())
+        one = torch.empty(T, H * D, dtype=kind, device="cuda")
+        F.ufp4_cache_read(cfg, c, slots, None, one, bool(rht))
+        assert torch.equal(one, want[1].to(kind))
+        F.ufp4_cache_read(cfg, c, slots, one, None, bool(rht))
+        assert torch.equal(one, want[0].to(kind))
