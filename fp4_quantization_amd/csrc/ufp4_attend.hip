@@ -15,11 +15,13 @@
 // (ufp4_expand.hpp); head scales, softmax scale and each row's power of two are
 // applied to fp32 logits and sums.
 //
-// The tokens of a sequence are cut into pieces of equal length, one a workgroup;
-// four waves share a piece's tiles and join in LDS, and where a sequence has
-// several pieces they meet through the workspace in a second kernel.  The length
-// of a piece follows from all lengths, read on the device, so that a batch of any
-// lengths fills the device evenly and the launch does not depend on them.
+// Work is counted in steps of 128 tokens (a tile of 32 for each of four waves) of
+// one unit, that is a sequence, key head and tile of rows.  All units' steps in a
+// row are cut into equal runs, one a workgroup, from the lengths, on the device: a
+// batch of any lengths fills the device evenly, and the launch does not depend on
+// them.  A workgroup answers the units that lie inside its run itself; a unit that
+// crosses into other runs leaves partial results in the workspace (at most two a
+// workgroup), which a second kernel joins.
 #include "ufp4_expand.hpp"
 #include "ufp4_serve.hpp"
 #include "ufp4_vec.hpp"
@@ -31,8 +33,9 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAtWaves = 4, kAtThreads = 64 * kAtWaves;
-constexpr int kMinPiece = 128;  // tokens: a tile for each wave
-constexpr int kMaxTokens = 1 << 30;  // of a sequence
+// Waves a SIMD holds of the kernel, which gives a wave 256 registers or 512.
+constexpr int attend_waves(int dt, int r) { return dt > 128 && r > 1 ? 1 : 2; }
+constexpr int kStep = 32 * kAtWaves;  // tokens
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
@@ -42,7 +45,7 @@ __device__ __forceinline__ float head_scale(const float* ts, int h) {
   return s > 0.0f && s <= 3.40282347e38f ? s : 1.0f;
 }
 
-// ---------------------------------------------------------------- pieces
+// ---------------------------------------------------------------- the runs
 struct Sequence {
   int64_t row0;  // of q
   int32_t n;     // drafted tokens
@@ -51,91 +54,100 @@ struct Sequence {
 };
 __device__ __forceinline__ Sequence sequence_of(const AttendParams& p, int b) {
   const int64_t r0 = p.q_offsets[b], r1 = p.q_offsets[b + 1];
+  const int len = p.lengths[b];
   const int64_t most = p.ld_pages * p.c.page_tokens;
   Sequence s{r0, 0, 0, 0};
   if (r0 < 0 || r1 < r0 || r1 > p.q_rows) return s;
   s.n = (int32_t)(r1 - r0);
   s.rows = (s.n < p.max_draft ? s.n : p.max_draft) * p.group;
-  const int len = p.lengths[b];
   s.len = len < 0 ? 0 : (len > most ? (int32_t)most : len);
   return s;
 }
-__device__ __forceinline__ int tiles_of(const Sequence& s, int rows) { return (s.rows + rows - 1) / rows; }
-// Pieces of a sequence: at least one for each head and tile of rows, so that a
-// sequence without tokens is answered too.
-__device__ __forceinline__ int splits_of(const Sequence& s, int piece) {
-  return s.len > 0 ? (s.len + piece - 1) / piece : 1;
-}
-
-// Sum over the workgroup of one value a thread.
-__device__ __forceinline__ int64_t block_sum(int64_t v, int64_t* red) {
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) v += __shfl_xor(v, d);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
-  __syncthreads();
-  v = 0;
-#pragma unroll
-  for (int w = 0; w < kAtWaves; ++w) v += red[w];
-  return v;
-}
-
-// Tokens a piece: the work of all sequences (tokens x tiles of rows x heads)
-// over the number of pieces aimed at, in whole tiles for every wave.
+// Steps of one unit of a sequence: one at least, so that a sequence without tokens
+// is answered too.
+__device__ __forceinline__ int unit_steps(const Sequence& s) { return s.len > kStep ? (s.len + kStep - 1) / kStep : 1; }
 template <int ROWS>
-__device__ __forceinline__ int piece_tokens(const AttendParams& p, int64_t* red) {
-  int64_t work = 0;
-  for (int b = threadIdx.x; b < p.sequences; b += kAtThreads) {
-    const Sequence s = sequence_of(p, b);
-    work += (int64_t)s.len * tiles_of(s, ROWS);
-  }
-  work = block_sum(work, red) * p.c.heads;
-  const int64_t t = (work + p.target - 1) / p.target;
-  if (t >= kMaxTokens) return kMaxTokens;
-  return t == 0 ? kMinPiece : (int)((t + kMinPiece - 1) / kMinPiece * kMinPiece);
+__device__ __forceinline__ int units_of(const AttendParams& p, const Sequence& s) {
+  return (s.rows + ROWS - 1) / ROWS * p.c.heads;
 }
 
-struct Piece {
-  int32_t b, first;  // sequence, and the first piece of it
-  int32_t index;     // among its pieces
+// A workgroup's run of steps, and the sequence that it begins in.
+struct Run {
+  int64_t lo, hi;  // steps
+  int64_t each;    // steps a run
+  int64_t first;   // the sequence's first step
+  int32_t b;
 };
-// The sequence that piece `id` belongs to, b = -1 past the last one.
 template <int ROWS>
-__device__ Piece find_piece(const AttendParams& p, int id, int piece, int32_t* sh) {
-  int before = 0;
+__device__ Run run_of(const AttendParams& p, int64_t* sh) {
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // sums of up to 256 sequences' steps are kept for the search; more are read again
+  int64_t mine = 0, total = 0;
+  for (int b = tid; b < p.sequences; b += kAtThreads) {
+    const Sequence s = sequence_of(p, b);
+    const int64_t n = (int64_t)unit_steps(s) * units_of<ROWS>(p, s);
+    if (b < kAtThreads) mine = n;
+    total += n;
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) total += __shfl_xor(total, d);
+  if (lane == 0) sh[wave] = total;
+  if (tid == 0) sh[kAtWaves] = -1;
+  __syncthreads();
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kAtWaves; ++w) total += sh[w];
+  Run r;
+  r.each = (total + gridDim.x - 1) / gridDim.x;
+  if (r.each < p.min_steps) r.each = p.min_steps;
+  r.lo = blockIdx.x * r.each;
+  r.hi = r.lo + r.each < total ? r.lo + r.each : total;
+  r.b = -1;
+  r.first = 0;
+  if (r.lo >= r.hi) return r;
+  int64_t before = 0;
   for (int b0 = 0; b0 < p.sequences; b0 += kAtThreads) {
-    const int b = b0 + threadIdx.x, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    int n = 0;
-    if (b < p.sequences) {
-      const Sequence s = sequence_of(p, b);
-      n = splits_of(s, piece) * tiles_of(s, ROWS) * p.c.heads;
+    if (b0 > 0) {
+      const Sequence s = sequence_of(p, b0 + tid < p.sequences ? b0 + tid : 0);
+      mine = b0 + tid < p.sequences ? (int64_t)unit_steps(s) * units_of<ROWS>(p, s) : 0;
     }
-    int inc = n;
+    int64_t inc = mine;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-      const int o = __shfl_up(inc, d);
+      const int64_t o = __shfl_up(inc, d);
       if (lane >= d) inc += o;
     }
     __syncthreads();
     if (lane == 63) sh[wave] = inc;
-    if (threadIdx.x == 0) sh[kAtWaves] = -1;
     __syncthreads();
-    int total = 0;
+    int64_t all = 0;
 #pragma unroll
     for (int w = 0; w < kAtWaves; ++w) {
       if (w < wave) inc += sh[w];
-      total += sh[w];
+      all += sh[w];
     }
-    const int first = before + inc - n;
-    if (id >= first && id < first + n) {
-      sh[kAtWaves] = b;
-      sh[kAtWaves + 1] = first;
+    const int64_t at = before + inc - mine;
+    if (r.lo >= at && r.lo < at + mine) {
+      sh[kAtWaves] = b0 + tid;
+      sh[kAtWaves + 1] = at;
     }
     __syncthreads();
-    if (sh[kAtWaves] >= 0) return Piece{uniform(sh[kAtWaves]), uniform(sh[kAtWaves + 1]), id - uniform(sh[kAtWaves + 1])};
-    before += total;
+    if (sh[kAtWaves] >= 0) {
+      r.b = (int)sh[kAtWaves];
+      r.first = sh[kAtWaves + 1];
+      return r;
+    }
+    before += all;
   }
-  return Piece{-1, 0, 0};
+  return r;
+}
+
+// Largest of the four lane groups' values of a column.
+__device__ __forceinline__ float max_of_groups(float v) {
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = fmaxf(__uint_as_float(a[0]), __uint_as_float(a[1]));
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(b[0]), __uint_as_float(b[1]));
 }
 
 // ---------------------------------------------------------------- values
@@ -190,13 +202,24 @@ __device__ __forceinline__ void scales_of(uint32_t four, f16x2& s01, f16x2& s23)
 }
 
 // ---------------------------------------------------------------- rows of q
-// A lane's part of row `row` of a tile (dim DT / 4 values from g DT / 4 on), as
-// fp16 fragments: q times a power of two for the row that takes its largest
-// magnitude to [2^12, 2^13) (its transform below 2^15), and with the transform a
-// second part, what the first one's rounding left.  Returns the power's exponent.
+// The folded signs of the transform (RhtSigns), in LDS: as scalars they would occupy
+// 16 registers through the whole loop.
+struct Signs {
+  float q1[8], q2[4], q3[2], q4, fin;
+};
+// Sign j of the transform from its mask (bit j set: -1).
+__device__ __forceinline__ float sign_of(uint32_t mask, int j) { return (mask >> j) & 1 ? -1.0f : 1.0f; }
+
+// One wave's 16 rows of a tile as fp16 fragments in LDS (lane (r, g): dim DT / 4
+// values of row r from g DT / 4 on): q times a power of two for the row that takes
+// its largest magnitude to [2^12, 2^13) (its transform below 2^15), and with the
+// transform a second part, what the first one's rounding left.  Returns the
+// power's exponent.
 template <int DT, int PARTS>
-__device__ __forceinline__ int load_q(const AttendParams& p, const uint16_t* q, bool in, int g, f16x8 (&f)[PARTS][DT / 32]) {
+__device__ __forceinline__ int prepare_q(int dim, const Signs& S, const uint16_t* q, bool in, int lane,
+                                         f16x8 (*to)[DT / 32][64]) {
   constexpr int N = DT / 4;
+  const int g = lane >> 4;
   float v[N];
 #pragma unroll
   for (int i = 0; i < N / 16; ++i) {
@@ -204,7 +227,7 @@ __device__ __forceinline__ int load_q(const AttendParams& p, const uint16_t* q, 
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       V8 a{};
-      if (in && d < p.c.dim) a = row_load(q + d + 8 * h, 8);
+      if (in && d < dim) a = row_load(q + d + 8 * h, 8);
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[16 * i + 8 * h + j] = a.v[j];
     }
@@ -224,28 +247,37 @@ __device__ __forceinline__ int load_q(const AttendParams& p, const uint16_t* q, 
   if (shift > 126) shift = 126;
   const float f2 = __uint_as_float((uint32_t)(shift + 127) << 23);
 #pragma unroll
-  for (int i = 0; i < N / 16; ++i) {
-    float* x = v + 16 * i;
+  for (int j = 0; j < N; ++j) v[j] *= f2;
+  if (PARTS == 2) {
+    RhtSigns sg;
 #pragma unroll
-    for (int j = 0; j < 16; ++j) x[j] *= f2;
-    if (PARTS == 2) {
-      fwht16_inlane(x, p.sg);
+    for (int k = 0; k < 8; ++k) sg.q1[k] = S.q1[k];
 #pragma unroll
-      for (int j = 0; j < 16; ++j) x[j] *= p.sg.fin;
+    for (int k = 0; k < 4; ++k) sg.q2[k] = S.q2[k];
+    sg.q3[0] = S.q3[0];
+    sg.q3[1] = S.q3[1];
+    sg.q4 = S.q4;
+    const float fin = S.fin;
+#pragma unroll
+    for (int i = 0; i < N / 16; ++i) {
+      fwht16_inlane(v + 16 * i, sg);
+#pragma unroll
+      for (int j = 0; j < 16; ++j) v[16 * i + j] *= fin;
     }
   }
 #pragma unroll
-  for (int i = 0; i < DT / 32; ++i)
+  for (int i = 0; i < DT / 32; ++i) {
+    f16x8 hi, lo;
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const float x = v[8 * i + j];
-      const _Float16 a = (_Float16)x;
-      f[0][i][j] = a;
-      if (PARTS == 2) {
-        const float left = x - (float)a;
-        f[PARTS - 1][i][j] = (_Float16)(left - left == 0.0f ? left : 0.0f);
-      }
+      hi[j] = (_Float16)x;
+      const float left = x - (float)hi[j];
+      lo[j] = (_Float16)(left - left == 0.0f ? left : 0.0f);
     }
+    to[0][i][lane] = hi;
+    if (PARTS == 2) to[PARTS - 1][i][lane] = lo;
+  }
   return shift;
 }
 
@@ -254,7 +286,8 @@ __device__ __forceinline__ int load_q(const AttendParams& p, const uint16_t* q, 
 // values 32 t + 8 g + j.  Inverse transform of the 16-block that lanes g and g ^ 1
 // share: three stages in the lane, one across, 1/4, signs.
 template <int NT>
-__device__ __forceinline__ void untransform(const AttendParams& p, float (&o)[NT][8], int g) {
+__device__ __forceinline__ void untransform(uint32_t mask, float (&o)[NT][8], int g) {
+  const uint32_t mine = mask >> (8 * (g & 1));
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
     float* v = o[t];
@@ -271,33 +304,34 @@ __device__ __forceinline__ void untransform(const AttendParams& p, float (&o)[NT
     for (int j = 0; j < 8; ++j) {
       const float other = __shfl_xor(v[j], 16);
       const float s = (g & 1) ? other - v[j] : v[j] + other;
-      v[j] = s * (0.25f * ((g & 1) ? p.d[8 + j] : p.d[j]));
+      v[j] = s * (0.25f * sign_of(mine, j));
     }
   }
 }
 
 // A finished row: O / l, tensor scale, inverse transform, out and lse.
+// The first value is column `col` of the head.
 template <int NT>
 __device__ __forceinline__ void finish_row(const AttendParams& p, float (&o)[NT][8], float m, float l, float vscale, bool in,
-                                           int64_t row, int head, int g) {
+                                           int64_t row, int head, int col, int g) {
   const float f = l > 0.0f || l != l ? vscale / l : 0.0f;
 #pragma unroll
   for (int t = 0; t < NT; ++t)
 #pragma unroll
     for (int j = 0; j < 8; ++j) o[t][j] *= f;
-  if (p.rht) untransform<NT>(p, o, g);
+  if (p.rht) untransform<NT>(p.signs, o, g);
   if (!in) return;
-  uint16_t* out = p.out + row * p.ldo + (int64_t)head * p.c.dim + 8 * g;
+  uint16_t* out = p.out + row * p.ldo + (int64_t)head * p.c.dim + col + 8 * g;
 #pragma unroll
   for (int t = 0; t < NT; ++t) {
-    if (32 * t < p.c.dim) {
+    if (col + 32 * t < p.c.dim) {
       V8 a;
 #pragma unroll
       for (int j = 0; j < 8; ++j) a.v[j] = o[t][j];
       store_16(out + 32 * t, pack(a));
     }
   }
-  if (p.lse && g == 0)
+  if (p.lse && col == 0 && g == 0)
     p.lse[row * p.q_heads + head] = l > 0.0f || l != l ? (m + __log2f(l)) * kLn2 : -__builtin_inff();
 }
 
@@ -305,313 +339,424 @@ template <int GRID>
 constexpr float unshift() { return (float)(1 << kExpandShift<GRID>); }
 
 // ---------------------------------------------------------------- the kernel
-template <int GRID, int DT, int R, int PARTS>
-__global__ __launch_bounds__(kAtThreads) void ufp4_attend_kernel(AttendParams p) {
+// What a wave reads of a tile of 32 tokens: this lane's parts of two keys (row r
+// of the first product's two tiles of 16) and of the values.
+template <int DT>
+struct Tile {
+  static constexpr int kWords = DT == 64 ? 2 : 4, kParts = (DT + 127) / 128, NT = DT / 32;
+  uint32_t kc[2][kParts][kWords], ks[2][kParts];
+  v32x2 vc[NT], vs[NT];
+};
+// A lane's byte offsets inside a tile of each array.  FULL: dim is DT; else parts of
+// a key past dim get an offset that is outside every tile, and read as zeros.
+template <int DT, bool FULL>
+struct Offsets {
+  static constexpr int kParts = Tile<DT>::kParts;
+  uint32_t kc[FULL ? 1 : kParts], ks[FULL ? 1 : kParts], vc, vs;
+  __device__ __forceinline__ Offsets(int dim, int g, int r) {
+    const int tok = 8 * (r >> 2) + (r & 3);
+#pragma unroll
+    for (int c = 0; c < (FULL ? 1 : kParts); ++c) {
+      const int d = g * (DT / 4) + 32 * c;
+      const bool in = FULL || d < dim;
+      kc[c] = in ? (uint32_t)(tok * (FULL ? DT : dim) + d) / 2 : 0x80000000u;
+      ks[c] = in ? (uint32_t)(tok * (FULL ? DT : dim) + d) / 16 : 0x80000000u;
+    }
+    vc = (uint32_t)(r * 32 + 8 * g);
+    vs = (uint32_t)((r >> 3) * 32 + 8 * g);
+  }
+};
+// The tile whose first token has index `at` in its cache (page, head, token); !ok:
+// nothing is read.
+template <int DT, bool FULL>
+__device__ __forceinline__ void load_tile(const AttendParams& p, int64_t at, bool ok, const Offsets<DT, FULL>& off, Tile<DT>& x) {
+  const int half = FULL ? DT / 2 : p.c.dim / 2, blocks = FULL ? DT / 16 : p.c.dim / 16;
+  const int bytes = ok ? kCacheTile * half : 0, sbytes = ok ? kCacheTile * blocks : 0;
+  // word 3: 32-bit data, raw addressing
+  const auto kc = __builtin_amdgcn_make_buffer_rsrc(p.c.kc + at * half, 0, bytes, 0x00020000);
+  const auto ks = __builtin_amdgcn_make_buffer_rsrc(p.c.ks + at * blocks, 0, sbytes, 0x00020000);
+  const auto vc = __builtin_amdgcn_make_buffer_rsrc(p.c.vc + at * half, 0, bytes, 0x00020000);
+  const auto vs = __builtin_amdgcn_make_buffer_rsrc(p.c.vs + at * blocks, 0, sbytes, 0x00020000);
+#pragma unroll
+  for (int u = 0; u < 2; ++u)
+#pragma unroll
+    for (int c = 0; c < Tile<DT>::kParts; ++c) {
+      const int ko = (int)(FULL ? off.kc[0] + 16 * c + 4 * u * half : off.kc[FULL ? 0 : c]), ks0 = FULL ? 0 : 4 * u * half;
+      const int so = (int)(FULL ? off.ks[0] + 2 * c + 4 * u * blocks : off.ks[FULL ? 0 : c]), ss0 = FULL ? 0 : 4 * u * blocks;
+      if constexpr (DT == 64) {
+        const v32x2 w = __builtin_bit_cast(v32x2, __builtin_amdgcn_raw_buffer_load_b64(kc, ko, ks0, 0));
+        x.kc[u][c][0] = w.x;
+        x.kc[u][c][1] = w.y;
+        x.ks[u][c] = __builtin_amdgcn_raw_buffer_load_b8(ks, so, ss0, 0);
+      } else {
+        const v32x4 w = __builtin_bit_cast(v32x4, __builtin_amdgcn_raw_buffer_load_b128(kc, ko, ks0, 0));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x.kc[u][c][j] = w[j];
+        x.ks[u][c] = __builtin_amdgcn_raw_buffer_load_b16(ks, so, ss0, 0);
+      }
+    }
+#pragma unroll
+  for (int t = 0; t < DT / 32; ++t) {
+    x.vc[t] = __builtin_bit_cast(v32x2, __builtin_amdgcn_raw_buffer_load_b64(vc, (int)off.vc + 512 * t, 0, 0));
+    x.vs[t] = __builtin_bit_cast(v32x2, __builtin_amdgcn_raw_buffer_load_b64(vs, (int)off.vs + 64 * t, 0, 0));
+  }
+}
+
+template <int GRID, int DT, int R, int PARTS, bool FULL>
+__global__ __launch_bounds__(kAtThreads, attend_waves(DT, R)) void ufp4_attend_kernel(AttendParams p) {
   constexpr int ROWS = 16 * R, NT = DT / 32;
   constexpr int kPitch = DT + 4;
-  __shared__ int64_t red[kAtWaves];
-  __shared__ int32_t sh[kAtWaves + 2];
+  // fragments of q that fit 32 registers stay in them, else they are read from LDS
+  // for every two tiles of 16 tokens
+  constexpr bool kInLds = R * NT >= 8;
+  __shared__ Signs S;
+  __shared__ f16x8 ql[R][PARTS][NT][64];
+  __shared__ int qshift[ROWS];
+  __shared__ int64_t sh[kAtWaves + 2];
   __shared__ float ml[kAtWaves][2][ROWS];
   __shared__ float join[2][ROWS][kPitch];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, g = lane >> 4, r = lane & 15;
-  const int piece = uniform(piece_tokens<ROWS>(p, red));
-  if (blockIdx.x == 0 && tid == 0) p.plan[0] = piece;
-  const Piece w = find_piece<ROWS>(p, (int)blockIdx.x, piece, sh);
-  if (w.b < 0) return;
-  const Sequence s = sequence_of(p, w.b);
-  const int splits = splits_of(s, piece);
-  // pieces of a sequence: [tile of rows][head][split]
-  const int split = w.index % splits, h = w.index / splits % p.c.heads, tile = w.index / splits / p.c.heads;
-  const int hist = s.len - s.n;  // below 0: drafted tokens that the cache does not hold
-  const int t_begin = split * piece, t_end = t_begin + piece < s.len ? t_begin + piece : s.len;
-
-  f16x8 qf[R][PARTS][NT];
-  float f[R];         // logits from sums, times log2 e
-  int drafted[R];     // of this lane's row
-  uint64_t bits[R];   // drafted tokens it sees
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int m = tile * ROWS + 16 * i + r;
-    const bool in = m < s.rows;
-    drafted[i] = m / p.group;
-    const int64_t row = s.row0 + drafted[i];
-    const int head = h * p.group + m % p.group;
-    const int shift = load_q<DT, PARTS>(p, p.q + (in ? row * p.ldq + (int64_t)head * p.c.dim : 0), in, g, qf[i]);
-    f[i] = (float)(pow2d(-shift) * (double)(unshift<GRID>() * kLog2e) * (double)p.scale * (double)head_scale(p.c.kts, h));
-    bits[i] = in && p.mask ? p.mask[row] : 0;
+  if (tid < 8) {
+    const uint32_t m = p.signs;
+    S.q1[tid] = sign_of(m, 2 * tid) * sign_of(m, 2 * tid + 1);
+    if (tid < 4) S.q2[tid] = sign_of(m, 4 * tid) * sign_of(m, 4 * tid + 2);
+    if (tid < 2) S.q3[tid] = sign_of(m, 8 * tid) * sign_of(m, 8 * tid + 4);
+    if (tid == 0) {
+      S.q4 = sign_of(m, 0) * sign_of(m, 8);
+      S.fin = 0.25f * sign_of(m, 0);
+    }
   }
-  f32x4 o[R][2 * NT];
-  float mx[R], sum[R];
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    mx[i] = -__builtin_inff();
-    sum[i] = 0.0f;
-#pragma unroll
-    for (int t = 0; t < 2 * NT; ++t) o[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  }
-  const int half = p.c.dim / 2, blocks = p.c.dim / 16;
-  const int key = 8 * (r >> 2) + (r & 3);  // token of row r of the first tile of 16
+  const Offsets<DT, FULL> off(p.c.dim, g, r);
+  const Run run = run_of<ROWS>(p, sh);
+  SplitUnit split{0, 0, 0, 0};
+  int64_t lo = run.lo;
+  int b = uniform(run.b);
+  int64_t first = run.first;
+  while (lo < run.hi) {
+    const Sequence s = sequence_of(p, b);
+    const int steps = unit_steps(s), units = units_of<ROWS>(p, s);
+    if (lo >= first + (int64_t)steps * units) {  // behind this sequence
+      first += (int64_t)steps * units;
+      ++b;
+      continue;
+    }
+    // units of a sequence: [head][tile of rows]
+    const int unit = uniform((int)((lo - first) / steps)), tiles = units / p.c.heads;
+    const int h = unit / tiles, tile = unit - h * tiles;
+    const int64_t unit_lo = first + (int64_t)unit * steps;
+    const int step0 = uniform((int)(lo - unit_lo));
+    const int step1 = uniform((int)(run.hi < unit_lo + steps ? run.hi - unit_lo : steps));
+    const int hist = s.len - s.n;  // below 0: drafted tokens that the cache does not hold
+    const int32_t* table = p.table + b * p.ld_pages;
 
-  for (int t0 = t_begin + 32 * wave; t0 < t_end; t0 += 32 * kAtWaves) {
-    const uint32_t slot = p.c.page.div((uint32_t)t0);
-    const int page = uniform(p.table[w.b * p.ld_pages + slot]);
-    if (page < 0 || page >= p.c.pages) continue;
-    const int64_t at = ((int64_t)page * p.c.heads + h) * p.c.page_tokens + (t0 - (int)slot * p.c.page_tokens);
-    const uint8_t* kc = p.c.kc + at * half;
-    const uint8_t* ks = p.c.ks + at * blocks;
-    const uint8_t* vc = p.c.vc + at * half;
-    const uint8_t* vs = p.c.vs + at * blocks;
-    // ---- logits
-    f32x4 a[R][2];
+    f32x4 o[R][2 * NT];
+    float mx[R], sum[R];
 #pragma unroll
-    for (int i = 0; i < R; ++i) a[i][0] = a[i][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < R; ++i) {
+      mx[i] = -__builtin_inff();
+      sum[i] = 0.0f;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-      const int tok = key + 4 * u;
+      for (int t = 0; t < 2 * NT; ++t) o[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    }
+
+    // this wave's tiles: the page of the one after the next is read, the next one
+    // is on its way, this one is computed
+    auto page_of = [&](int step) {
+      const int t0 = step * kStep + 32 * wave;
+      return step < step1 && t0 < s.len ? uniform(table[p.c.page.div((uint32_t)t0)]) : -1;
+    };
+    auto fetch = [&](int step, int page, Tile<DT>& x) {
+      const bool ok = page >= 0 && page < p.c.pages;
+      const int t0 = step * kStep + 32 * wave;
+      const int in_page = t0 - (int)p.c.page.div((uint32_t)t0) * p.c.page_tokens;
+      load_tile<DT, FULL>(p, ok ? ((int64_t)page * p.c.heads + h) * p.c.page_tokens + in_page : 0, ok, off, x);
+      return ok;
+    };
+    Tile<DT> next;
+    bool next_ok = fetch(step0, page_of(step0), next);
+    int page = page_of(step0 + 1);
+
+    // rows of q, by one wave for each 16
+    if (wave < R) {
+      const int m = tile * ROWS + 16 * wave + r;
+      const bool in = m < s.rows;
+      const uint16_t* q = p.q + (in ? (s.row0 + m / p.group) * p.ldq + (int64_t)(h * p.group + m % p.group) * p.c.dim : 0);
+      const int shift = prepare_q<DT, PARTS>(p.c.dim, S, q, in, lane, ql[wave]);
+      if (g == 0) qshift[16 * wave + r] = shift;
+    }
+    __syncthreads();
+    f16x8 qf[kInLds ? 1 : R][PARTS][NT];
+    float f[R];        // logits from sums, times log2 e
+    int drafted[R];    // of this lane's row
+    uint64_t bits[R];  // drafted tokens it sees
 #pragma unroll
-      for (int c = 0; c < (DT + 127) / 128; ++c) {
-        // up to 32 codes of the key and their one or two scales
-        const int d = g * (DT / 4) + 32 * c;
-        constexpr int W = DT == 64 ? 2 : 4;
-        uint32_t codes[4] = {0u, 0u, 0u, 0u}, two = 0;
-        if (d < p.c.dim) {
-          if (W == 2) {
-            const v32x2 x = *reinterpret_cast<const v32x2*>(kc + tok * half + d / 2);
-            codes[0] = x.x;
-            codes[1] = x.y;
-            two = ks[tok * blocks + d / 16];
-          } else {
-            const v32x4 x = *reinterpret_cast<const v32x4*>(kc + tok * half + d / 2);
+    for (int i = 0; i < R; ++i) {
+      const int m = tile * ROWS + 16 * i + r;
+      drafted[i] = m / p.group;
+      f[i] = (float)(pow2d(-qshift[16 * i + r]) * (double)(unshift<GRID>() * kLog2e) * (double)p.scale *
+                     (double)head_scale(p.c.kts, h));
+      bits[i] = m < s.rows && p.mask ? p.mask[s.row0 + drafted[i]] : 0;
+      if constexpr (!kInLds) {
 #pragma unroll
-            for (int j = 0; j < 4; ++j) codes[j] = x[j];
-            two = *reinterpret_cast<const uint16_t*>(ks + tok * blocks + d / 16);
+        for (int q = 0; q < PARTS; ++q)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) qf[i][q][t] = ql[i][q][t][lane];
+      }
+    }
+
+    for (int step = step0; step < step1; ++step) {
+      const Tile<DT> x = next;
+      const bool ok = next_ok;
+      next_ok = fetch(step + 1, page, next);
+      page = page_of(step + 2);
+      if (!ok) continue;
+      const int t0 = step * kStep + 32 * wave;
+      // ---- logits
+      f32x4 a[R][2];
+#pragma unroll
+      for (int i = 0; i < R; ++i) a[i][0] = a[i][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int c = 0; c < Tile<DT>::kParts; ++c) {
+        const f16x2 ds[2] = {expand_scales<GRID>(x.ks[0][c] & 0x7F7Fu), expand_scales<GRID>(x.ks[1][c] & 0x7F7Fu)};
+#pragma unroll
+        for (int j = 0; j < Tile<DT>::kWords; ++j) {
+          f16x8 kf[2];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            uint32_t e[4];
+            expand8_shifted<GRID>(x.kc[u][c][j], j < 2 ? f16x2{ds[u].x, ds[u].x} : f16x2{ds[u].y, ds[u].y}, e);
+            kf[u] = __builtin_bit_cast(f16x8, g32x4{e[0], e[1], e[2], e[3]});
           }
-        }
-        const f16x2 ds = expand_scales<GRID>(two & 0x7F7Fu);
-#pragma unroll
-        for (int j = 0; j < W; ++j) {
-          uint32_t e[4];
-          expand8_shifted<GRID>(codes[j], j < 2 ? f16x2{ds.x, ds.x} : f16x2{ds.y, ds.y}, e);
-          const f16x8 kf = __builtin_bit_cast(f16x8, g32x4{e[0], e[1], e[2], e[3]});
 #pragma unroll
           for (int i = 0; i < R; ++i)
 #pragma unroll
-            for (int q = 0; q < PARTS; ++q)
-              a[i][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf, qf[i][q][4 * c + j], a[i][u], 0, 0, 0);
+            for (int q = 0; q < PARTS; ++q) {
+              f16x8 y;
+              if constexpr (kInLds) y = ql[i][q][4 * c + j][lane];
+              else y = qf[i][q][4 * c + j];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) a[i][u] = __builtin_amdgcn_mfma_f32_16x16x32_f16(kf[u], y, a[i][u], 0, 0, 0);
+            }
         }
       }
-    }
-    // ---- softmax: this lane's tokens are t0 + 8 g + j
-    const bool edge = t0 + 32 > hist;  // the wave's
-    uint32_t alive = 0xFF;             // tokens that exist
-    f16x8 pf[R];
-#pragma unroll
-    for (int i = 0; i < R; ++i) {
-      float x[8];
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = a[i][j >> 2][j & 3] * f[i];
-      if (edge) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int t = t0 + 8 * g + j, d = t - hist;
-          const bool seen = t < s.len && (d < 0 || (p.mask ? d < 64 && ((bits[i] >> d) & 1) : d <= drafted[i]));
-          x[j] = seen ? x[j] : -__builtin_inff();
-        }
-      }
-      float m = x[0];
-#pragma unroll
-      for (int j = 1; j < 8; ++j) m = fmaxf(m, x[j]);
-      m = fmaxf(m, __shfl_xor(m, 16));
-      m = fmaxf(m, __shfl_xor(m, 32));
-      m = fmaxf(m, mx[i]);
-      const float base = m == -__builtin_inff() ? 0.0f : m;
-      const float alpha = __builtin_amdgcn_exp2f(mx[i] - base);
-      float l = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const float e = __builtin_amdgcn_exp2f(x[j] - base);
-        l += e;
-        pf[i][j] = (_Float16)e;
-      }
-      sum[i] = sum[i] * alpha + l;
-      if (__any(alpha != 1.0f)) {
-#pragma unroll
-        for (int t = 0; t < 2 * NT; ++t) o[i][t] *= alpha;
-      }
-      mx[i] = m;
-    }
-    if (edge) {
-      const int left = s.len - t0 - 8 * g;
-      alive = left >= 8 ? 0xFFu : left <= 0 ? 0u : (1u << left) - 1u;
-    }
-    // ---- values
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      if (32 * t >= p.c.dim) break;
-      const v32x2 c = *reinterpret_cast<const v32x2*>(vc + (16 * t + r) * 32 + 8 * g);
-      v32x2 b = *reinterpret_cast<const v32x2*>(vs + (2 * t + (r >> 3)) * 32 + 8 * g) & 0x7F7F7F7Fu;
-      if (edge) {
-        // tokens that do not exist hold anything
-        uint32_t k0 = 0, k1 = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          k0 |= (alive >> j) & 1 ? 0xFFu << (8 * j) : 0u;
-          k1 |= (alive >> (4 + j)) & 1 ? 0xFFu << (8 * j) : 0u;
-        }
-        b.x &= k0;
-        b.y &= k1;
-      }
-      f16x2 s01, s23, s45, s67;
-      scales_of<GRID>(b.x, s01, s23);
-      scales_of<GRID>(b.y, s45, s67);
-      uint32_t first[4], second[4];
-      expand_tokens<GRID>(c.x, s01, s23, first, second);
-      expand_tokens<GRID>(c.y, s45, s67, first + 2, second + 2);
-      const f16x8 v0 = __builtin_bit_cast(f16x8, g32x4{first[0], first[1], first[2], first[3]});
-      const f16x8 v1 = __builtin_bit_cast(f16x8, g32x4{second[0], second[1], second[2], second[3]});
+      // ---- softmax: this lane's tokens are t0 + 8 g + j
+      const bool edge = t0 + 32 > hist;  // the wave's
+      f16x8 pf[R];
 #pragma unroll
       for (int i = 0; i < R; ++i) {
-        o[i][2 * t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[i], o[i][2 * t], 0, 0, 0);
-        o[i][2 * t + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[i], o[i][2 * t + 1], 0, 0, 0);
-      }
-    }
-  }
-
-  // ---- the waves' results join: common maximum, then two and two
+        float y[8];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    sum[i] += __shfl_xor(sum[i], 16);
-    sum[i] += __shfl_xor(sum[i], 32);
-    if (g == 0) {
-      ml[wave][0][16 * i + r] = mx[i];
-      ml[wave][1][16 * i + r] = sum[i];
-    }
-  }
-  __syncthreads();
-  float acc[R][NT][8];
+        for (int j = 0; j < 8; ++j) y[j] = a[i][j >> 2][j & 3] * f[i];
+        if (edge) {
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    float m = -__builtin_inff(), l = 0.0f;
-#pragma unroll
-    for (int k = 0; k < kAtWaves; ++k) m = fmaxf(m, ml[k][0][16 * i + r]);
-    const float base = m == -__builtin_inff() ? 0.0f : m;
-#pragma unroll
-    for (int k = 0; k < kAtWaves; ++k) l += ml[k][1][16 * i + r] * __builtin_amdgcn_exp2f(ml[k][0][16 * i + r] - base);
-    const float alpha = __builtin_amdgcn_exp2f(mx[i] - base);
-    mx[i] = m;
-    sum[i] = l;
-    // values 32 t + 8 g + 2 k + parity, from row 4 g + k of the two tiles
-#pragma unroll
-    for (int t = 0; t < NT; ++t)
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        acc[i][t][2 * k] = o[i][2 * t][k] * alpha;
-        acc[i][t][2 * k + 1] = o[i][2 * t + 1][k] * alpha;
-      }
-  }
-#pragma unroll
-  for (int step = kAtWaves / 2; step >= 1; step >>= 1) {
-    if (wave >= step && wave < 2 * step) {
-#pragma unroll
-      for (int i = 0; i < R; ++i)
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          float* to = &join[wave - step][16 * i + r][32 * t + 8 * g];
-#pragma unroll
-          for (int j = 0; j < 8; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{acc[i][t][j], acc[i][t][j + 1], acc[i][t][j + 2], acc[i][t][j + 3]};
+          for (int j = 0; j < 8; ++j) {
+            const int t = t0 + 8 * g + j, d = t - hist;
+            const bool chosen = p.mask ? (d < 64) & (int)((bits[i] >> (d & 63)) & 1) : d <= drafted[i];
+            const bool seen = (t < s.len) & ((d < 0) | chosen);
+            y[j] = seen ? y[j] : -__builtin_inff();
+          }
         }
+        float m = y[0];
+#pragma unroll
+        for (int j = 1; j < 8; ++j) m = fmaxf(m, y[j]);
+        m = fmaxf(max_of_groups(m), mx[i]);
+        const float base = m == -__builtin_inff() ? 0.0f : m;
+        const float alpha = __builtin_amdgcn_exp2f(mx[i] - base);
+        float l = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float e = __builtin_amdgcn_exp2f(y[j] - base);
+          l += e;
+          pf[i][j] = (_Float16)e;
+        }
+        sum[i] = sum[i] * alpha + l;
+        if (__any(alpha != 1.0f)) {
+#pragma unroll
+          for (int t = 0; t < 2 * NT; ++t) o[i][t] *= alpha;
+        }
+        mx[i] = m;
+      }
+      // ---- values
+      uint32_t keep0 = 0x7F7F7F7Fu, keep1 = 0x7F7F7F7Fu;
+      if (edge) {
+        // tokens that do not exist hold anything: their scales become 0
+        const int left = s.len - t0 - 8 * g;
+        if (left < 8) keep1 = left <= 4 ? 0u : keep1 >> (8 * (8 - left));
+        if (left < 4) keep0 = left <= 0 ? 0u : keep0 >> (8 * (4 - left));
+      }
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (!FULL && 32 * t >= p.c.dim) break;
+        f16x2 s01, s23, s45, s67;
+        scales_of<GRID>(x.vs[t].x & keep0, s01, s23);
+        scales_of<GRID>(x.vs[t].y & keep1, s45, s67);
+        uint32_t v0[4], v1[4];
+        expand_tokens<GRID>(x.vc[t].x, s01, s23, v0, v1);
+        expand_tokens<GRID>(x.vc[t].y, s45, s67, v0 + 2, v1 + 2);
+        const f16x8 even = __builtin_bit_cast(f16x8, g32x4{v0[0], v0[1], v0[2], v0[3]});
+        const f16x8 odd = __builtin_bit_cast(f16x8, g32x4{v1[0], v1[1], v1[2], v1[3]});
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+          o[i][2 * t] = __builtin_amdgcn_mfma_f32_16x16x32_f16(even, pf[i], o[i][2 * t], 0, 0, 0);
+          o[i][2 * t + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(odd, pf[i], o[i][2 * t + 1], 0, 0, 0);
+        }
+      }
+    }
+
+    // ---- the waves' results join: common maximum, then two and two
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      sum[i] += __shfl_xor(sum[i], 16);
+      sum[i] += __shfl_xor(sum[i], 32);
+      if (g == 0) {
+        ml[wave][0][16 * i + r] = mx[i];
+        ml[wave][1][16 * i + r] = sum[i];
+      }
     }
     __syncthreads();
-    if (wave < step) {
+    float acc[R][NT][8];
 #pragma unroll
-      for (int i = 0; i < R; ++i)
+    for (int i = 0; i < R; ++i) {
+      float m = -__builtin_inff(), l = 0.0f;
 #pragma unroll
-        for (int t = 0; t < NT; ++t)
+      for (int k = 0; k < kAtWaves; ++k) m = fmaxf(m, ml[k][0][16 * i + r]);
+      const float base = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
-          for (int j = 0; j < 8; ++j) acc[i][t][j] += join[wave][16 * i + r][32 * t + 8 * g + j];
-    }
-    __syncthreads();
-  }
-  if (wave != 0) return;
-  const float vscale = head_scale(p.c.vts, h) * unshift<GRID>();
-#pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const int m = tile * ROWS + 16 * i + r;
-    if (splits == 1) {
-      finish_row<NT>(p, acc[i], mx[i], sum[i], vscale, m < s.rows, s.row0 + m / p.group, h * p.group + m % p.group, g);
-    } else {
-      const int64_t at = (int64_t)blockIdx.x * ROWS + 16 * i + r;
-      if (g == 0) p.ml[at] = make_float2(mx[i], sum[i]);
+      for (int k = 0; k < kAtWaves; ++k) l += ml[k][1][16 * i + r] * __builtin_amdgcn_exp2f(ml[k][0][16 * i + r] - base);
+      const float alpha = __builtin_amdgcn_exp2f(mx[i] - base);
+      mx[i] = m;
+      sum[i] = l;
+      // values 32 t + 8 g + 2 k + parity, from row 4 g + k of the two tiles
 #pragma unroll
       for (int t = 0; t < NT; ++t)
-        if (32 * t < p.c.dim) {
-          float* to = p.o + at * p.c.dim + 32 * t + 8 * g;
 #pragma unroll
-          for (int j = 0; j < 8; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{acc[i][t][j], acc[i][t][j + 1], acc[i][t][j + 2], acc[i][t][j + 3]};
+        for (int k = 0; k < 4; ++k) {
+          acc[i][t][2 * k] = o[i][2 * t][k] * alpha;
+          acc[i][t][2 * k + 1] = o[i][2 * t + 1][k] * alpha;
         }
     }
+#pragma unroll
+    for (int half = kAtWaves / 2; half >= 1; half >>= 1) {
+      if (wave >= half && wave < 2 * half) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int t = 0; t < NT; ++t) {
+            float* to = &join[wave - half][16 * i + r][32 * t + 8 * g];
+#pragma unroll
+            for (int j = 0; j < 8; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{acc[i][t][j], acc[i][t][j + 1], acc[i][t][j + 2], acc[i][t][j + 3]};
+          }
+      }
+      __syncthreads();
+      if (wave < half) {
+#pragma unroll
+        for (int i = 0; i < R; ++i)
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int j = 0; j < 8; ++j) acc[i][t][j] += join[wave][16 * i + r][32 * t + 8 * g + j];
+      }
+      __syncthreads();
+    }
+    const bool whole = step0 == 0 && step1 == steps;
+    if (wave == 0) {
+      const float vscale = head_scale(p.c.vts, h) * unshift<GRID>();
+      const int64_t slot = 2 * (int64_t)blockIdx.x + (step0 == 0 ? 1 : 0);
+#pragma unroll
+      for (int i = 0; i < R; ++i) {
+        const int m = tile * ROWS + 16 * i + r;
+        if (whole) {
+          finish_row<NT>(p, acc[i], mx[i], sum[i], vscale, m < s.rows, s.row0 + m / p.group, h * p.group + m % p.group, 0, g);
+        } else {
+          const int64_t at = slot * ROWS + 16 * i + r;
+          if (g == 0) p.ml[at] = make_float2(mx[i], sum[i]);
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+            if (FULL || 32 * t < p.c.dim) {
+              float* to = p.o + at * p.c.dim + 32 * t + 8 * g;
+#pragma unroll
+              for (int j = 0; j < 8; j += 4) *reinterpret_cast<f32x4*>(to + j) = f32x4{acc[i][t][j], acc[i][t][j + 1], acc[i][t][j + 2], acc[i][t][j + 3]};
+            }
+        }
+      }
+    }
+    // the unit goes on in the runs behind this one
+    if (!whole && step0 == 0) split = SplitUnit{b, h, tile, (int32_t)((unit_lo + steps - 1) / run.each - blockIdx.x + 1)};
+    lo = unit_lo + step1;
   }
+  if (tid == 0 && p.split) p.split[blockIdx.x] = split;
 }
 
-// Joins the pieces of a sequence: one wave takes 16 rows of a tile and head,
-// blockIdx.y the sequence.
-template <int GRID, int DT, int R>
+// Joins the partial results of the unit that begins in run blockIdx.x and ends in a
+// later one: 16 rows and 32 columns a workgroup, whose waves share the runs.
+template <int GRID, int R>
 __global__ __launch_bounds__(kAtThreads) void ufp4_attend_join_kernel(AttendParams p) {
-  constexpr int ROWS = 16 * R, NT = DT / 32;
-  __shared__ int64_t red[kAtWaves];
-  const int b = blockIdx.y, piece = uniform(p.plan[0]);
-  const Sequence s = sequence_of(p, b);
-  const int splits = splits_of(s, piece), tiles = tiles_of(s, ROWS);
-  if (splits == 1 || tiles == 0) return;
-  int64_t before = 0;
-  for (int i = threadIdx.x; i < b; i += kAtThreads) {
-    const Sequence o = sequence_of(p, i);
-    before += (int64_t)splits_of(o, piece) * tiles_of(o, ROWS) * p.c.heads;
-  }
-  before = block_sum(before, red);
+  constexpr int ROWS = 16 * R;
+  __shared__ float ml[kAtWaves][2][64];
+  __shared__ float part[kAtWaves][64][8 + 1];
+  const SplitUnit u = p.split[blockIdx.x];
+  if (u.runs == 0) return;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-  const int unit = (int)blockIdx.x * kAtWaves + wave;  // [tile][head][16 rows]
-  const int part = unit % R, h = unit / R % p.c.heads, tile = unit / R / p.c.heads;
-  if (tile >= tiles) return;
-  const int64_t first = ((before + ((int64_t)tile * p.c.heads + h) * splits) * ROWS) + 16 * part + r;
+  const int i = blockIdx.y % R, col = blockIdx.y / R * 32;
+  // run k of the unit is slot 1 of its first workgroup and slot 0 of the others
+  auto row_of = [&](int k) { return (2 * ((int64_t)blockIdx.x + k) + (k == 0)) * ROWS + 16 * i + r; };
   float m = -__builtin_inff(), l = 0.0f;
-  for (int k = 0; k < splits; ++k) m = fmaxf(m, p.ml[first + (int64_t)k * ROWS].x);
+  for (int k = wave; k < u.runs; k += kAtWaves) m = fmaxf(m, p.ml[row_of(k)].x);
+  ml[wave][0][lane] = m;
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < kAtWaves; ++k) m = fmaxf(m, ml[k][0][lane]);
   const float base = m == -__builtin_inff() ? 0.0f : m;
-  float o[NT][8];
+  float o[1][8];
 #pragma unroll
-  for (int t = 0; t < NT; ++t)
-#pragma unroll
-    for (int j = 0; j < 8; ++j) o[t][j] = 0.0f;
-  for (int k = 0; k < splits; ++k) {
-    const int64_t at = first + (int64_t)k * ROWS;
+  for (int j = 0; j < 8; ++j) o[0][j] = 0.0f;
+#pragma unroll 4
+  for (int k = wave; k < u.runs; k += kAtWaves) {
+    const int64_t at = row_of(k);
     const float2 x = p.ml[at];
+    const f32x4* from = reinterpret_cast<const f32x4*>(p.o + at * p.c.dim + col + 8 * g);
+    const f32x4 y0 = from[0], y1 = from[1];
     const float alpha = __builtin_amdgcn_exp2f(x.x - base);
     l += x.y * alpha;
 #pragma unroll
-    for (int t = 0; t < NT; ++t)
-      if (32 * t < p.c.dim) {
-        const float* from = p.o + at * p.c.dim + 32 * t + 8 * g;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) o[t][j] += from[j] * alpha;
-      }
+    for (int j = 0; j < 4; ++j) {
+      o[0][j] += y0[j] * alpha;
+      o[0][4 + j] += y1[j] * alpha;
+    }
   }
-  const int q = tile * ROWS + 16 * part + r;
-  finish_row<NT>(p, o, m, l, head_scale(p.c.vts, h) * unshift<GRID>(), q < s.rows, s.row0 + q / p.group,
-                 h * p.group + q % p.group, g);
+  ml[wave][1][lane] = l;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) part[wave][lane][j] = o[0][j];
+  __syncthreads();
+  if (wave != 0) return;
+#pragma unroll
+  for (int k = 1; k < kAtWaves; ++k) {
+    l += ml[k][1][lane];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) o[0][j] += part[k][lane][j];
+  }
+  const Sequence s = sequence_of(p, u.b);
+  const int q = u.tile * ROWS + 16 * i + r;
+  finish_row<1>(p, o, m, l, head_scale(p.c.vts, u.h) * unshift<GRID>(), q < s.rows, s.row0 + q / p.group,
+                u.h * p.group + q % p.group, col, g);
 }
 
 template <int GRID, int DT, int R>
-hipError_t launch_rows(const AttendParams& p, hipStream_t s) {
+hipError_t launch_rows(const AttendParams& p0, hipStream_t s) {
+  AttendParams p = p0;
   // no sequence is longer than its line of the page table
-  const int64_t most = (p.ld_pages * p.c.page_tokens + kMinPiece - 1) / kMinPiece;
-  const int64_t units = (int64_t)p.sequences * p.c.heads * p.row_tiles;
-  const int64_t pieces = units * (most > 0 ? most : 1) < p.max_pieces ? units * (most > 0 ? most : 1) : p.max_pieces;
-  if (p.rht) ufp4_attend_kernel<GRID, DT, R, 2><<<(unsigned)pieces, kAtThreads, 0, s>>>(p);
-  else ufp4_attend_kernel<GRID, DT, R, 1><<<(unsigned)pieces, kAtThreads, 0, s>>>(p);
+  const int64_t cap = (p.ld_pages * p.c.page_tokens + kStep - 1) / kStep, steps = cap > 0 ? cap : 1;
+  const int64_t units = (int64_t)p.sequences * p.c.heads * p.row_tiles, most = units * steps;
+  const unsigned runs = (unsigned)(most < p.max_runs ? most : p.max_runs);
+  p.min_steps = 1;
+  const bool full = p.c.dim == DT;
+  if (p.rht && full) ufp4_attend_kernel<GRID, DT, R, 2, true><<<runs, kAtThreads, 0, s>>>(p);
+  else if (p.rht) ufp4_attend_kernel<GRID, DT, R, 2, false><<<runs, kAtThreads, 0, s>>>(p);
+  else if (full) ufp4_attend_kernel<GRID, DT, R, 1, true><<<runs, kAtThreads, 0, s>>>(p);
+  else ufp4_attend_kernel<GRID, DT, R, 1, false><<<runs, kAtThreads, 0, s>>>(p);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || most <= 1) return e;
-  const unsigned gx = (unsigned)(((int64_t)p.row_tiles * p.c.heads * R + kAtWaves - 1) / kAtWaves);
-  ufp4_attend_join_kernel<GRID, DT, R><<<dim3(gx, (unsigned)p.sequences), kAtThreads, 0, s>>>(p);
+  if (e != hipSuccess || steps == 1) return e;
+  ufp4_attend_join_kernel<GRID, R><<<dim3(runs, (unsigned)(R * (p.c.dim / 32))), kAtThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 
@@ -627,9 +772,9 @@ hipError_t launch_grid(const AttendParams& p, hipStream_t s) {
 
 int attend_rows(int32_t dim, int32_t group, int32_t max_draft) { return (int64_t)group * max_draft > 16 ? 32 : 16; }
 
-int64_t attend_max_pieces(int32_t heads, int32_t row_tiles, int32_t sequences) {
-  return kAttendTarget + (int64_t)sequences * heads * row_tiles;
-}
+// Runs of a launch: the workgroups that 256 compute units hold at once (one where
+// a wave takes more than half of the registers).
+int32_t attend_runs(int32_t dim, int32_t rows) { return dim > 128 && rows > 16 ? 256 : 512; }
 
 hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
   switch (p.grid) {

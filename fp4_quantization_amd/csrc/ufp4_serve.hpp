@@ -69,11 +69,15 @@ hipError_t launch_cache_append(const CacheParams& p, hipStream_t s);
 hipError_t launch_cache_read(const CacheParams& p, hipStream_t s);
 
 // ------------------------------------------------------------------ attention
+// A unit of attention (a sequence, key head and tile of rows) that begins in a run
+// and ends in a later one; runs: how many it lies in, 0: there is none.
+struct SplitUnit {
+  int32_t b, h, tile, runs;
+};
 struct AttendParams {
   CacheView c;
   int32_t grid, rht;
-  RhtSigns sg;
-  float d[16];
+  uint32_t signs;  // of the transform, bit j set: -1
   const uint16_t* q;
   uint16_t* out;
   float* lse;
@@ -86,19 +90,16 @@ struct AttendParams {
   int32_t sequences, max_draft;
   const uint64_t* mask;
   float scale;
-  // work is cut into pieces of one sequence's tokens, one key head and one tile
-  // of rows; partial results of pieces go to the workspace
-  int32_t row_tiles;   // of a sequence with max_draft drafted tokens
-  int64_t max_pieces;  // of a launch
-  int32_t target;      // pieces aimed at
-  int32_t* plan;       // [0]: tokens a piece
-  float2* ml;          // [piece][row]: maximum and sum
-  float* o;            // [piece][row][dim]
+  int32_t row_tiles;  // of a sequence with max_draft drafted tokens
+  int32_t max_runs;   // of a launch
+  int32_t min_steps;  // of a run
+  SplitUnit* split;   // [run]
+  float2* ml;         // [run][2][row]: maximum and sum
+  float* o;           // [run][2][row][dim]
 };
-// Rows (drafted tokens x query heads) of a tile, and pieces of a launch.
+// Rows (drafted tokens x query heads) of a tile, and the most runs of a launch.
 int attend_rows(int32_t dim, int32_t group, int32_t max_draft);
-int64_t attend_max_pieces(int32_t heads, int32_t row_tiles, int32_t sequences);
-constexpr int kAttendTarget = 1024;
+int32_t attend_runs(int32_t dim, int32_t rows);
 hipError_t launch_attend(const AttendParams& p, hipStream_t s);
 
 }  // namespace ufp4

@@ -70,8 +70,9 @@ int cache_view(const ufp4_cache* c, CacheView& v) {
   return UFP4_OK;
 }
 
-size_t attend_ws(int64_t pieces, int rows, int dim) {
-  return 256 + (size_t)pieces * rows * sizeof(float2) + (size_t)pieces * rows * dim * sizeof(float);
+// Two partial results a run.
+size_t attend_ws(int runs, int rows, int dim) {
+  return (size_t)runs * (sizeof(SplitUnit) + 2 * (size_t)rows * (sizeof(float2) + dim * sizeof(float)));
 }
 
 }  // namespace
@@ -183,9 +184,7 @@ size_t ufp4_tree_attention_workspace(const ufp4_cache* cache, int32_t q_heads, i
       sequences > kMaxSequences || max_draft < 1 || max_draft >= kMaxRows / q_heads)
     return 0;
   const int group = q_heads / cache->heads, rows = attend_rows(cache->dim, group, max_draft);
-  const int64_t tiles = ((int64_t)max_draft * group + rows - 1) / rows;
-  const int64_t pieces = attend_max_pieces(cache->heads, (int32_t)tiles, sequences);
-  return pieces < ((int64_t)1 << 24) ? attend_ws(pieces, rows, cache->dim) : 0;
+  return attend_ws(attend_runs(cache->dim, rows), rows, cache->dim);
 }
 
 int ufp4_tree_attention(const ufp4_config* cfg, const ufp4_cache* cache, const uint16_t* q, int64_t ldq,
@@ -216,7 +215,7 @@ int ufp4_tree_attention(const ufp4_config* cfg, const ufp4_cache* cache, const u
   if (!ws || ws_bytes < need || !aligned(ws, 16)) return UFP4_ERR_WORKSPACE;
   p.grid = cfg->grid;
   p.rht = cfg->rht != 0;
-  signs_of(cfg, p.sg, p.d);
+  p.signs = rht_sign_mask(cfg->rht_seed);
   p.q = q;
   p.out = out;
   p.lse = lse;
@@ -235,12 +234,12 @@ int ufp4_tree_attention(const ufp4_config* cfg, const ufp4_cache* cache, const u
   p.scale = softmax_scale;
   const int rows = attend_rows(cache->dim, p.group, max_draft);
   p.row_tiles = (int32_t)(((int64_t)max_draft * p.group + rows - 1) / rows);
-  p.max_pieces = attend_max_pieces(cache->heads, p.row_tiles, sequences);
-  p.target = kAttendTarget;
+  p.max_runs = attend_runs(cache->dim, rows);
   uint8_t* at = static_cast<uint8_t*>(ws);
-  p.plan = reinterpret_cast<int32_t*>(at);
-  p.ml = reinterpret_cast<float2*>(at + 256);
-  p.o = reinterpret_cast<float*>(at + 256 + (size_t)p.max_pieces * rows * sizeof(float2));
+  p.split = reinterpret_cast<SplitUnit*>(at);
+  at += (size_t)p.max_runs * sizeof(SplitUnit);
+  p.ml = reinterpret_cast<float2*>(at);
+  p.o = reinterpret_cast<float*>(at + (size_t)p.max_runs * 2 * rows * sizeof(float2));
   return done(launch_attend(p, (hipStream_t)stream));
 }
 
