@@ -23,6 +23,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kMvWaves = 8, kMvThreads = 64 * kMvWaves;
+constexpr int kSegment = 4;  // chunks of a wave whose weights are on the way at once
 constexpr int kLdsTokens = 4;
 constexpr size_t kLdsX = 96 << 10;  // bytes
 
@@ -124,10 +125,8 @@ __device__ __forceinline__ void store_parts(const float v[16], uint16_t* xp, int
 }
 
 template <bool MX, int PARTS>
-__device__ __forceinline__ void prepare_block(const MatvecParams& p, int64_t t, int64_t k, int shift, uint16_t* xp, int TP,
+__device__ __forceinline__ void prepare_block(const MatvecParams& p, float v[16], int64_t k, int shift, uint16_t* xp, int TP,
                                               int at) {
-  float v[16];
-  load_block(p, t, k, v);
   if (!MX) {
     const float f = pow2f(shift);
 #pragma unroll
@@ -141,31 +140,37 @@ __device__ __forceinline__ void prepare_block(const MatvecParams& p, int64_t t, 
   store_parts<MX, PARTS>(v, xp, k, TP, at);
 }
 
-// One workgroup a token of a whole number of 16; the last ones are zeros.
+// blockIdx.x: a token of a whole number of 16 (the last ones are zeros); blockIdx.y:
+// a part of its values, after the token's maximum, which every part finds itself.
+constexpr int kPrepareThreads = 256;
 template <bool MX, int PARTS>
-__global__ __launch_bounds__(1024) void ufp4_matvec_prepare_kernel(MatvecParams p) {
-  __shared__ uint32_t top;
+__global__ __launch_bounds__(kPrepareThreads) void ufp4_matvec_prepare_kernel(MatvecParams p) {
+  __shared__ uint32_t top[kPrepareThreads / 64];
   const int64_t t = blockIdx.x, K = (p.K + kMvChunk - 1) / kMvChunk * kMvChunk;
   int shift = 0;
   if (!MX) {
-    if (threadIdx.x == 0) top = 0;
-    __syncthreads();
     uint32_t m = 0;
-    for (int64_t k = threadIdx.x * 16; k < p.K; k += blockDim.x * 16) {
+    for (int64_t k = threadIdx.x * 16; k < p.K; k += kPrepareThreads * 16) {
       float v[16];
       load_block(p, t, k, v);
       const uint32_t b = block_max(v);
       m = m > b ? m : b;
     }
     m = wave_max(m);
-    if ((threadIdx.x & 63) == 0) atomicMax(&top, m);
+    if ((threadIdx.x & 63) == 0) top[threadIdx.x >> 6] = m;
     __syncthreads();
-    shift = shift_of(top, p.rht);
+#pragma unroll
+    for (int w = 0; w < kPrepareThreads / 64; ++w) m = m > top[w] ? m : top[w];
+    shift = shift_of(m, p.rht);
   }
-  if (threadIdx.x == 0 && t < p.tokens) p.shift[t] = shift;
+  if (threadIdx.x == 0 && blockIdx.y == 0 && t < p.tokens) p.shift[t] = shift;
   uint16_t* xp = p.xp + (size_t)(t / 16) * (K / kMvChunk) * PARTS * 16 * kMvChunk;
-  for (int64_t k = threadIdx.x * 16; k < K; k += blockDim.x * 16)
-    prepare_block<MX, PARTS>(p, t, k, shift, xp, 16, (int)(t % 16));
+  for (int64_t k = (blockIdx.y * kPrepareThreads + threadIdx.x) * 16; k < K; k += (int64_t)gridDim.y * kPrepareThreads * 16)
+  {
+    float v[16];
+    load_block(p, t, k, v);
+    prepare_block<MX, PARTS>(p, v, k, shift, xp, 16, (int)(t % 16));
+  }
 }
 
 // ---------------------------------------------------------------- weights
@@ -191,36 +196,76 @@ __device__ __forceinline__ void expand8_mx(uint32_t w, float scale, uint32_t out
   out[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(b, scale, true));
 }
 
-// 32 codes of a row and their scale bytes.
-struct Granule {
-  v32x4 c;
-  uint32_t s;
+// A lane's part of a segment of up to kSegment chunks of 128 values, of row r: 32 codes
+// of each chunk (those of its group g), and the scales of all groups of chunk g,
+// which one load of 8 (MX32: 4) bytes brings where loads of 2 (1) for each chunk
+// took 10 of 71 us (65536 x 8192).  Where a row's scales are not whole words (APART)
+// they are loaded for each chunk all the same: the last word would lie half behind
+// the array.
+struct Segment {
+  v32x4 c[kSegment];
+  uint32_t s[kSegment];
+};
+// Up to 16 rows of w from row `row` on; what lies past them (or past the end of a
+// row, by an offset of kOutside) reads as zeros.
+constexpr uint32_t kOutside = 0x80000000u;
+struct Rows {
+  __amdgpu_buffer_rsrc_t codes, scales;
 };
 template <bool MX>
-__device__ __forceinline__ Granule load_granule(const uint8_t* codes, const uint8_t* scales, int64_t k, bool in) {
-  Granule w{v32x4{0u, 0u, 0u, 0u}, 0u};
-  if (in) {
-    w.c = *reinterpret_cast<const v32x4*>(codes + k / 2);
-    w.s = MX ? (uint32_t)scales[k / 32] : (uint32_t)*reinterpret_cast<const uint16_t*>(scales + k / 16);
-  }
-  return w;
+__device__ __forceinline__ Rows rows_of(const MatvecParams& p, int64_t row) {
+  const int64_t left = p.N - row;
+  const uint32_t n = left <= 0 ? 0u : left < 16 ? (uint32_t)left : 16u;
+  const int64_t at = n ? row * p.K : 0;
+  const uint32_t values = n * (uint32_t)p.K;
+  // word 3: 32-bit data, raw addressing
+  return Rows{__builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.codes + at / 2), 0, (int)(values / 2), 0x00020000),
+              __builtin_amdgcn_make_buffer_rsrc(const_cast<uint8_t*>(p.scales + at / (MX ? 32 : 16)), 0,
+                                                (int)(values / (MX ? 32 : 16)), 0x00020000)};
 }
+// The scales of this lane's codes in chunks 0 .. 3: the 4 x 4 transposition over the
+// lane groups of what they loaded.  NV16: two bytes each (low half of s[i]).
+template <bool MX, bool APART>
+__device__ __forceinline__ void own_scales(const Segment& w, int g, uint32_t (&s)[kSegment]) {
+  if (APART) {
+#pragma unroll
+    for (int j = 0; j < kSegment; ++j) s[j] = w.s[j];
+  } else if (MX) {
+    const auto h = __builtin_amdgcn_permlane32_swap(w.s[0], w.s[0], false, false);  // chunk g & 1, and 2 more
+    const auto a = __builtin_amdgcn_permlane16_swap(h[0], h[0], false, false);
+    const auto b = __builtin_amdgcn_permlane16_swap(h[1], h[1], false, false);
+    s[0] = (a[0] >> (8 * g)) & 0xFFu;
+    s[1] = (a[1] >> (8 * g)) & 0xFFu;
+    s[2] = (b[0] >> (8 * g)) & 0xFFu;
+    s[3] = (b[1] >> (8 * g)) & 0xFFu;
+  } else {
+    // groups g & 2 and its next of the chunks g & 1 (h[0]) and (g & 1) + 2 (h[1])
+    const auto h = __builtin_amdgcn_permlane32_swap(w.s[0], w.s[1], false, false);
+    const uint32_t even = __builtin_amdgcn_perm(h[1], h[0], 0x05040100u), odd = __builtin_amdgcn_perm(h[1], h[0], 0x07060302u);
+    const auto o = __builtin_amdgcn_permlane16_swap(even, odd, false, false);
+    s[0] = o[0];
+    s[1] = o[1];
+    s[2] = o[0] >> 16;
+    s[3] = o[1] >> 16;
+  }
+}
+// 32 codes and their scale bytes as four fragments.
 template <int GRID, bool MX>
-__device__ __forceinline__ void expand_granule(const Granule& w, v32x4 f[4]) {
+__device__ __forceinline__ void expand_granule(const v32x4& c, uint32_t s, v32x4 f[4]) {
   if (MX) {
-    const float scale = __uint_as_float(w.s << 23);
+    const float scale = __uint_as_float(s << 23);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t e[4];
-      expand8_mx<GRID>(w.c[i], scale, e);
+      expand8_mx<GRID>(c[i], scale, e);
       f[i] = v32x4{e[0], e[1], e[2], e[3]};
     }
   } else {
-    const f16x2 ds = expand_scales<GRID>(w.s & 0x7F7Fu);
+    const f16x2 ds = expand_scales<GRID>(s & 0x7F7Fu);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       uint32_t e[4];
-      expand8_shifted<GRID>(w.c[i], i < 2 ? f16x2{ds.x, ds.x} : f16x2{ds.y, ds.y}, e);
+      expand8_shifted<GRID>(c[i], i < 2 ? f16x2{ds.x, ds.x} : f16x2{ds.y, ds.y}, e);
       f[i] = v32x4{e[0], e[1], e[2], e[3]};
     }
   }
@@ -249,44 +294,111 @@ __device__ __forceinline__ void store_y(const MatvecParams& p, int64_t at, const
   }
 }
 
-// Rows of w in tiles of 16, walked over by the workgroups; a tile's values of K
-// are split over the waves, whose sums meet in LDS.  LDSX: up to four tokens,
-// prepared by every workgroup; else 16 NT of the tokens the kernel above prepared.
-template <int GRID, bool MX, int PARTS, int NT, bool LDSX>
-__global__ __launch_bounds__(kMvThreads) void ufp4_matvec_kernel(MatvecParams p) {
+// Where the fragments of x' come from: LDS, where every workgroup has prepared them
+// (up to four tokens); registers, read once from what the kernel above prepared
+// (one fragment a step, K of one segment); or that memory, tile by tile.
+enum XSource { kXLds, kXRegisters, kXMemory };
+
+// Rows of w in tiles of 16, walked over by the workgroups.  kw of the eight waves
+// share a tile's chunks of K, and their sums meet in LDS; 8 / kw tiles side by side.
+// A wave's weights are loaded a segment (four chunks) ahead of their use, the first
+// ones before x' is prepared.
+template <int GRID, bool MX, int PARTS, int NT, XSource X, bool APART>
+__global__ __launch_bounds__(kMvThreads, X == kXRegisters ? 2 : 4) void ufp4_matvec_kernel(MatvecParams p, int log_kw) {
   extern __shared__ v32x4 xs[];
   __shared__ f32x4 part[2][kMvWaves][NT][64];
   __shared__ uint32_t top[kLdsTokens];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, g = lane >> 4, r = lane & 15;
   const int chunks = (int)((p.K + kMvChunk - 1) / kMvChunk);
+  const int kw = 1 << log_kw, wk = wave & (kw - 1), wt = wave >> log_kw, side = kMvWaves >> log_kw;
+  const int segments = chunks > 0 ? (chunks + kSegment * kw - 1) / (kSegment * kw) : 1;
+  // neighbouring chunks of a wave's segment: 256 bytes of each row together
+  const int run = chunks < kSegment * kw ? (chunks + kw - 1) >> log_kw : kSegment;
+  auto chunk_of = [&](int segment, int j) { return j < run ? segment * kSegment * kw + wk * run + j : chunks; };
   const int64_t t0 = (int64_t)blockIdx.y * 16 * NT;
-  const int TP = LDSX ? (int)p.tokens : 16;
-  if (LDSX) {
+  const int TP = X == kXLds ? (int)p.tokens : 16;
+  const int tiles = (int)((p.N + 15) / 16), groups = (tiles + side - 1) / side;
+
+  // this wave's weights of a segment, row r of a tile
+  auto fetch = [&](int group, int segment, Segment& w) {
+    const Rows rows = rows_of<MX>(p, ((int64_t)group * side + wt) * 16);
+    const uint32_t line = (uint32_t)r * (uint32_t)p.K;
+#pragma unroll
+    for (int j = 0; j < kSegment; ++j) {
+      const uint32_t k = (uint32_t)chunk_of(segment, j) * kMvChunk + 32 * g;
+      w.c[j] = __builtin_bit_cast(v32x4, __builtin_amdgcn_raw_buffer_load_b128(
+                                             rows.codes, (int)(k < (uint32_t)p.K ? (line + k) / 2 : kOutside), 0, 0));
+    }
+    if (APART) {
+#pragma unroll
+      for (int j = 0; j < kSegment; ++j) {
+        const uint32_t k = (uint32_t)chunk_of(segment, j) * kMvChunk + 32 * g;
+        w.s[j] = MX ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(rows.scales, (int)(k < (uint32_t)p.K ? (line + k) / 32 : kOutside), 0, 0)
+                    : (uint32_t)__builtin_amdgcn_raw_buffer_load_b16(rows.scales, (int)(k < (uint32_t)p.K ? (line + k) / 16 : kOutside), 0, 0);
+      }
+      return;
+    }
+    const uint32_t k = (uint32_t)(segment * kSegment * kw + wk * run + g) * kMvChunk;
+    const bool in = g < run && k < (uint32_t)p.K;
+    if (MX) {
+      w.s[0] = __builtin_amdgcn_raw_buffer_load_b32(rows.scales, (int)(in ? (line + k) / 32 : kOutside), 0, 0);
+    } else {
+      const v32x2 x = __builtin_bit_cast(v32x2, __builtin_amdgcn_raw_buffer_load_b64(rows.scales, (int)(in ? (line + k) / 16 : kOutside), 0, 0));
+      w.s[0] = x.x;
+      w.s[1] = x.y;
+    }
+  };
+  // position (tile group and segment) of the next load.  Behind the last group
+  // nothing is read, without a branch: the compiler would wait for all loads where
+  // some may not have been made.
+  int load_group = blockIdx.x, load_segment = 0;
+  auto fetch_next = [&](Segment& w) {
+    fetch(load_group, load_segment, w);
+    const bool last = load_segment + 1 == segments;
+    load_segment = last ? 0 : load_segment + 1;
+    load_group += last ? (int)gridDim.x : 0;
+  };
+  Segment wa, wb;
+  if (X == kXLds) {
+    // blocks of 16 values: one a thread where that suffices, loaded ahead of the
+    // first weights (loads return in order)
+    const int blocks = chunks * (kMvChunk / 16), all = TP * blocks;
+    float v[16];
+    const int t1 = tid < all ? tid / blocks : 0, k1 = (tid - t1 * blocks) * 16;
+    if (tid < all) load_block(p, t1, k1, v);
+    fetch_next(wa);
     if (!MX) {
       if (tid < kLdsTokens) top[tid] = 0;
       __syncthreads();
-      for (int t = 0; t < TP; ++t) {
-        uint32_t m = 0;
-        for (int64_t k = tid * 16; k < p.K; k += kMvThreads * 16) {
-          float v[16];
-          load_block(p, t, k, v);
-          const uint32_t b = block_max(v);
-          m = m > b ? m : b;
+      for (int i = tid; i < all; i += kMvThreads) {
+        float u[16];
+        const int t = i / blocks;
+        if (i != tid) load_block(p, t, (i - t * blocks) * 16, u);
+        const uint32_t m = block_max(i != tid ? u : v);
+        // all lanes of a wave have one token where its blocks are a multiple of 64
+        if (blocks % 64 == 0) {
+          const uint32_t wm = wave_max(m);
+          if (lane == 0) atomicMax(&top[t], wm);
+        } else {
+          atomicMax(&top[t], m);
         }
-        m = wave_max(m);
-        if (lane == 0) atomicMax(&top[t], m);
       }
       __syncthreads();
     }
-    for (int t = 0; t < TP; ++t)
-      for (int64_t k = tid * 16; k < (int64_t)chunks * kMvChunk; k += kMvThreads * 16)
-        prepare_block<MX, PARTS>(p, t, k, MX ? 0 : shift_of(top[t], p.rht), reinterpret_cast<uint16_t*>(xs), TP, t);
+    for (int i = tid; i < all; i += kMvThreads) {
+      const int t = i / blocks, k = (i - t * blocks) * 16;
+      if (i != tid) load_block(p, t, k, v);
+      prepare_block<MX, PARTS>(p, v, k, MX ? 0 : shift_of(top[t], p.rht), reinterpret_cast<uint16_t*>(xs), TP, t);
+    }
     __syncthreads();
+  } else {
+    fetch_next(wa);
   }
+  fetch_next(wb);
   const v32x4* xf[NT];
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    if (LDSX) {
+    if (X == kXLds) {
       xf[n] = xs + g * TP + (r < TP ? r : TP - 1);
     } else {
       // past the last token's sixteen: any sixteen, whose results are not stored
@@ -294,67 +406,143 @@ __global__ __launch_bounds__(kMvThreads) void ufp4_matvec_kernel(MatvecParams p)
       xf[n] = reinterpret_cast<const v32x4*>(p.xp) + (size_t)t16 * chunks * PARTS * 4 * 64 + g * 16 + r;
     }
   }
-  constexpr float kUnshift = MX ? 1.0f : (float)(1 << kExpandShift<GRID>);
-  const int64_t tiles = (p.N + 15) / 16;
-  int buf = 0;
-  for (int64_t tile = blockIdx.x; tile < tiles; tile += gridDim.x, buf ^= 1) {
-    const int64_t row = tile * 16 + r < p.N ? tile * 16 + r : p.N - 1;
-    const uint8_t* codes = p.codes + row * (p.K / 2);
-    const uint8_t* scales = p.scales + row * (p.K / (MX ? 32 : 16));
-    f32x4 acc[NT];
+  auto piece = [&](int n, int c, int i, int q) { return xf[n][(((size_t)c * 4 + i) * PARTS + q) * 4 * TP]; };
+  v32x4 xr[X == kXRegisters ? kSegment : 1][4];
+  if (X == kXRegisters) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int c = wave; c < chunks; c += kMvWaves) {
-      const int64_t k = (int64_t)c * kMvChunk + 32 * g;
+    for (int j = 0; j < kSegment; ++j)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) xr[j][i] = piece(0, chunk_of(0, j) < chunks ? chunk_of(0, j) : 0, i, 0);
+  }
+  // what a sum is multiplied by, for each of this lane's tokens: in 64 bits, since
+  // neither the token's power of two nor S alone has to be in fp32's range
+  double factor[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    const int64_t t = t0 + 16 * n + r;
+    factor[n] = MX ? 1.0 : 0.0;
+    if (!MX && t < p.tokens && p.K > 0) {
+      const int shift = X == kXLds ? shift_of(top[r], p.rht) : p.shift[t];
+      factor[n] = pow2d(-shift) * (double)(1 << kExpandShift<GRID>) * (double)p.ts[0];
+    }
+  }
+  f32x4 acc[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) acc[n] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  int group = blockIdx.x, segment = 0, buf = 0;
+  // multiplies the segment in x and has the one after the next loaded in its place
+  auto step = [&](Segment& x) {
+    uint32_t scales[kSegment];
+    own_scales<MX, APART>(x, g, scales);
+#pragma unroll
+    for (int j = 0; j < kSegment; ++j) {
+      const int c = chunk_of(segment, j);
+      if (c >= chunks || group >= groups) break;
       v32x4 f[4];
-      expand_granule<GRID, MX>(load_granule<MX>(codes, scales, k, k < p.K), f);
+      // (past the end of a row its scale bytes are the next row's)
+      expand_granule<GRID, MX>(x.c[j], c * kMvChunk + 32 * g < (int)p.K ? scales[j] : 0u, f);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int q = 0; q < PARTS; ++q) acc[n] = mfma<MX>(f[i], xf[n][((size_t)c * 4 + i) * PARTS * 4 * TP + q * 4 * TP], acc[n]);
+          for (int q = 0; q < PARTS; ++q)
+            acc[n] = mfma<MX>(f[i], X == kXRegisters ? xr[X == kXRegisters ? j : 0][i] : piece(n, c, i, q), acc[n]);
     }
+    fetch_next(x);
+    const bool last = ++segment == segments;
+    if (!last || group >= groups) return;
+    // the tile's sums; a wave that has a tile of its own holds them already
+    if (kw > 1) {
 #pragma unroll
-    for (int n = 0; n < NT; ++n) part[buf][wave][n][lane] = acc[n];
-    __syncthreads();
-    if (wave < NT) {
-      f32x4 v = part[buf][0][wave][lane];
+      for (int n = 0; n < NT; ++n) part[buf][wave][n][lane] = acc[n];
+      __syncthreads();
+    }
+    const int tile = group * side + wt;
 #pragma unroll
-      for (int w = 1; w < kMvWaves; ++w) v += part[buf][w][wave][lane];
+    for (int i = 0; i < NT; ++i) {
+      f32x4 v = acc[i];
+      acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      if ((i & (kw - 1)) != wk) continue;
+      if (kw > 1) {
+        v = part[buf][wt << log_kw][i][lane];
+        for (int u = 1; u < kw; ++u) v += part[buf][(wt << log_kw) + u][i][lane];
+      }
       // a lane holds token r of the 16 and four neighbouring rows of w
-      const int64_t t = t0 + 16 * wave + r, n = tile * 16 + 4 * g;
+      const int64_t t = t0 + 16 * i + r, n = (int64_t)tile * 16 + 4 * g;
       if (t < p.tokens && n < p.N) {
-        const int shift = MX || p.K == 0 ? 0 : LDSX ? shift_of(top[r], p.rht) : p.shift[t];
-        // in 64 bits: neither factor alone has to be in fp32's range
-        const double s = pow2d(-shift) * (double)kUnshift * (MX || p.K == 0 ? 1.0 : (double)p.ts[0]);
+        if (!MX) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] = (float)((double)v[i] * s);
+          for (int e = 0; e < 4; ++e) v[e] = (float)((double)v[e] * factor[i]);
+        }
         store_y(p, t * p.ldy + n, v, p.N - n);
       }
     }
+    segment = 0;
+    group += gridDim.x;
+    buf ^= 1;
+  };
+  // two at a time, without an exit in between: where it met the loop's, the compiler
+  // would take each buffer's loads for the youngest and wait for both.  A step
+  // behind the last one does nothing.
+  const int steps = (groups - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x * segments;
+  for (int i = 0; i < steps; i += 2) {
+    step(wa);
+    step(wb);
   }
+}
+
+constexpr int kCus = 256;
+
+// Waves that share a tile: those that have a whole segment of K each, and more where
+// that leaves waves of the device (16 a compute unit) without work.  One token, N x K
+// = 65536 x 8192: 70 us with 1, 2, 4 or 8; 4096 x 4096: 19, 12.5, 9.5, 7.5; 16 tokens,
+// 16384 x 4096: 26.6, 15.7, 16.2, 14.3.
+int log_waves(int64_t tiles, int64_t chunks) {
+  int log_kw = 0;
+  while (log_kw < 3 && (kSegment << log_kw) < chunks) ++log_kw;
+  while (log_kw < 3 && (2 << log_kw) <= chunks && (tiles << log_kw) < 16 * kCus) ++log_kw;
+  return log_kw;
+}
+
+template <int GRID, bool MX, int PARTS, bool APART>
+hipError_t launch_apart(const MatvecParams& p, hipStream_t s) {
+  const int64_t tiles = (p.N + 15) / 16, chunks = (p.K + kMvChunk - 1) / kMvChunk;
+  const int log_kw = log_waves(tiles, chunks), side = kMvWaves >> log_kw;
+  const int64_t groups = (tiles + side - 1) / side;
+  const unsigned gx = (unsigned)(groups < 2 * kCus ? groups : 2 * kCus);
+  if (matvec_in_lds(p.tokens, p.K, PARTS)) {
+    const size_t lds = (size_t)chunks * kMvChunk * p.tokens * PARTS * 2;
+    ufp4_matvec_kernel<GRID, MX, PARTS, 1, kXLds, APART><<<gx, kMvThreads, lds, s>>>(p, log_kw);
+    return hipGetLastError();
+  }
+  const int64_t t16 = (p.tokens + 15) / 16;
+  if (p.K > 0) {
+    const int64_t parts = (p.K + 16 * kPrepareThreads - 1) / (16 * kPrepareThreads);
+    ufp4_matvec_prepare_kernel<MX, PARTS><<<dim3((unsigned)(16 * t16), (unsigned)(parts < 8 ? parts : 8)), kPrepareThreads, 0, s>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  // as many tokens a workgroup as leave every compute unit one
+  int nt = t16 > 2 ? 4 : (int)t16;
+  while (nt > 1 && groups * ((t16 + nt - 1) / nt) < kCus) nt /= 2;
+  const dim3 grid(gx, (unsigned)((t16 + nt - 1) / nt));
+  if (nt == 1 && PARTS == 1 && chunks <= (kSegment << log_kw)) {
+    const dim3 one(gx < kCus ? gx : kCus, grid.y);
+    if constexpr (PARTS == 1) ufp4_matvec_kernel<GRID, MX, PARTS, 1, kXRegisters, APART><<<one, kMvThreads, 0, s>>>(p, log_kw);
+  } else if (nt == 1) {
+    ufp4_matvec_kernel<GRID, MX, PARTS, 1, kXMemory, APART><<<grid, kMvThreads, 0, s>>>(p, log_kw);
+  } else if (nt == 2) {
+    ufp4_matvec_kernel<GRID, MX, PARTS, 2, kXMemory, APART><<<grid, kMvThreads, 0, s>>>(p, log_kw);
+  } else {
+    ufp4_matvec_kernel<GRID, MX, PARTS, 4, kXMemory, APART><<<grid, kMvThreads, 0, s>>>(p, log_kw);
+  }
+  return hipGetLastError();
 }
 
 template <int GRID, bool MX, int PARTS>
 hipError_t launch_grid(const MatvecParams& p, hipStream_t s) {
-  const int64_t tiles = (p.N + 15) / 16;
-  const unsigned gx = (unsigned)(tiles < 1024 ? tiles : 1024);
-  if (matvec_in_lds(p.tokens, p.K, PARTS)) {
-    const size_t lds = (size_t)((p.K + kMvChunk - 1) / kMvChunk) * kMvChunk * p.tokens * PARTS * 2;
-    ufp4_matvec_kernel<GRID, MX, PARTS, 1, true><<<gx, kMvThreads, lds, s>>>(p);
-    return hipGetLastError();
-  }
-  const unsigned t16 = (unsigned)((p.tokens + 15) / 16);
-  if (p.K > 0) {
-    ufp4_matvec_prepare_kernel<MX, PARTS><<<16 * t16, 1024, 0, s>>>(p);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  if (t16 == 1) ufp4_matvec_kernel<GRID, MX, PARTS, 1, false><<<gx, kMvThreads, 0, s>>>(p);
-  else if (t16 == 2) ufp4_matvec_kernel<GRID, MX, PARTS, 2, false><<<gx, kMvThreads, 0, s>>>(p);
-  else ufp4_matvec_kernel<GRID, MX, PARTS, 4, false><<<dim3(gx, (t16 + 3) / 4), kMvThreads, 0, s>>>(p);
-  return hipGetLastError();
+  return p.K % (MX ? 128 : 64) ? launch_apart<GRID, MX, PARTS, true>(p, s) : launch_apart<GRID, MX, PARTS, false>(p, s);
 }
 
 template <bool MX, int PARTS>
