@@ -569,35 +569,37 @@ def ufp4_gemm_grouped_dw(cfg: ufp4_config, a: QTensor, b: QTensor, offsets: torc
 
 # ---------------------------------------------------------------- decoding
 
-class _on_device_of:
-    """The device that all of the tensors lie on, as the current one, and the
-    stream of a call there (None: the device's current stream)."""
+_getDevice, _rawStream = torch._C._cuda_getDevice, torch._C._cuda_getCurrentRawStream
 
-    def __init__(self, stream, *tensors):
-        index = -1
-        for t in tensors:
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError("every tensor of the call must lie on the GPU")
-            if index >= 0 and t.get_device() != index:
-                raise ValueError("all tensors of the call must lie on one device")
-            index = t.get_device()
-        if stream is not None and stream.device_index != index:
-            raise ValueError("the stream must belong to the device of the tensors")
-        self.index, self.stream = index, stream
 
-    def __enter__(self) -> int:
-        self.before = torch._C._cuda_getDevice()
-        if self.before != self.index:
-            torch._C._cuda_setDevice(self.index)
-        if self.stream is not None:
-            return self.stream.cuda_stream
-        return torch._C._cuda_getCurrentRawStream(self.index)
+def _one_device(*tensors) -> int:
+    """The device that all of the tensors (or None) lie on."""
+    index = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != index:
+            raise ValueError("all tensors of the call must lie on one device")
+    if index < 0:
+        raise ValueError("every tensor of the call must lie on the GPU")
+    return index
 
-    def __exit__(self, *_):
-        if self.before != self.index:
-            torch._C._cuda_setDevice(self.before)
+
+def _call(name: str, device: int, stream, *args) -> None:
+    """Calls an entry point whose last argument is the stream (None: the current
+    stream of `device`), with `device` as the current one."""
+    if stream is None:
+        s = _rawStream(device)
+    elif stream.device_index == device:
+        s = stream.cuda_stream
+    else:
+        raise ValueError("the stream must belong to the device of the tensors")
+    fn = getattr(lib, name)
+    if _getDevice() == device:
+        rc = fn(*args, s)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, s)
+    if rc:
+        check(name, rc)
 
 
 class _Scratch:
@@ -607,10 +609,7 @@ class _Scratch:
     def __init__(self, nbytes: int, device):
         self.nbytes = int(nbytes)
         self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
-
-    @property
-    def ptr(self):
-        return _ptr(self.buf)
+        self.ptr = self.buf.data_ptr()
 
 
 class MatvecWorkspace(_Scratch):
@@ -631,15 +630,19 @@ def ufp4_matvec(cfg: ufp4_config, x: torch.Tensor, w: QTensor, y: torch.Tensor, 
     block = block_len(cfg.scaling)
     if rows != tokens:
         raise ValueError("x and y must have one row a token")
-    if (tuple(w.codes.shape) != (N, K // 2) or tuple(w.scales.shape) != (N, K // block) or not w.codes.is_contiguous()
-            or not w.scales.is_contiguous() or w.codes.element_size() != 1 or w.scales.element_size() != 1):
+    codes, scales = w.codes, w.scales
+    if (codes.shape != (N, K // 2) or scales.shape != (N, K // block) or not codes.is_contiguous()
+            or not scales.is_contiguous() or codes.element_size() != 1 or scales.element_size() != 1):
         raise ValueError(f"w must hold {N} contiguous lines of {K} codes and their scales, a byte each")
     if w.tensor_scale.dtype != torch.float32 or w.tensor_scale.numel() < 1:
         raise ValueError("w must have a float32 tensor scale")
-    with _on_device_of(stream, x, y, w.codes, w.scales, w.tensor_scale, ws.buf if ws else None) as s:
-        check("ufp4_matvec",
-              lib.ufp4_matvec(ctypes.byref(cfg), _ptr(x), xt, tokens, K, ldx, w.c(), N, _ptr(y), yt, ldy,
-                              ws.ptr if ws else None, ws.nbytes if ws else 0, s))
+    if ws is None:
+        ptr, nbytes = None, 0
+        device = _one_device(x, y, w.codes, w.scales, w.tensor_scale)
+    else:
+        ptr, nbytes = ws.ptr, ws.nbytes
+        device = _one_device(x, y, w.codes, w.scales, w.tensor_scale, ws.buf)
+    _call("ufp4_matvec", device, stream, cfg, x.data_ptr(), xt, tokens, K, ldx, w.c(), N, y.data_ptr(), yt, ldy, ptr, nbytes)
 
 
 class QCache:
@@ -663,13 +666,23 @@ class QCache:
         for t in (k_scale, v_scale):
             if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (heads,) or not t.is_contiguous()):
                 raise ValueError("tensor scales must be contiguous float32 [heads]")
-        self.k_codes, self.k_scales, self.v_codes, self.v_scales = k_codes, k_scales, v_codes, v_scales
-        self.k_scale, self.v_scale = k_scale, v_scale
         self.pages, self.heads, self.page_tokens, self.dim = pages, heads, tokens, 2 * half
-        self.tensors = (k_codes, k_scales, v_codes, v_scales, k_scale, v_scale)
+        # the buffers stay those of this object: their addresses are laid out once
+        self._tensors = (k_codes, k_scales, v_codes, v_scales, k_scale, v_scale)
+        self._c = ufp4_cache(*(_ptr(t) for t in self._tensors), pages, tokens, heads, 2 * half)
+        device = k_codes.get_device()
+        if any(t is not None and t.get_device() != device for t in self._tensors):
+            raise ValueError("all buffers of the cache must lie on one device")
+
+    k_codes = property(lambda self: self._tensors[0])
+    k_scales = property(lambda self: self._tensors[1])
+    v_codes = property(lambda self: self._tensors[2])
+    v_scales = property(lambda self: self._tensors[3])
+    k_scale = property(lambda self: self._tensors[4])
+    v_scale = property(lambda self: self._tensors[5])
 
     def c(self) -> ufp4_cache:
-        return ufp4_cache(*(_ptr(t) for t in self.tensors), self.pages, self.page_tokens, self.heads, self.dim)
+        return self._c
 
 
 def alloc_cache(pages: int, page_tokens: int, heads: int, dim: int, k_scale: torch.Tensor | None = None,
@@ -692,10 +705,8 @@ def ufp4_cache_append(cfg: ufp4_config, cache: QCache, k: torch.Tensor, v: torch
     vr, vcols, ldv = _bf16_rows(v, "v")
     if (cols, vr, vcols) != (cache.heads * cache.dim, rows, cols) or slots.numel() != rows:
         raise ValueError("k and v must be [tokens, heads * dim] with one slot a token")
-    with _on_device_of(stream, k, v, _int64(slots, "slots"), *cache.tensors) as s:
-        check("ufp4_cache_append",
-              lib.ufp4_cache_append(ctypes.byref(cfg), ctypes.byref(cache.c()), _ptr(k), ldk, _ptr(v), ldv, rows,
-                                    _ptr(slots), s))
+    _call("ufp4_cache_append", _one_device(k, v, _int64(slots, "slots"), cache.k_codes), stream, cfg, cache.c(), k.data_ptr(),
+          ldk, v.data_ptr(), ldv, rows, slots.data_ptr())
 
 
 def ufp4_cache_read(cfg: ufp4_config, cache: QCache, slots: torch.Tensor, k_out: torch.Tensor | None,
@@ -705,22 +716,21 @@ def ufp4_cache_read(cfg: ufp4_config, cache: QCache, slots: torch.Tensor, k_out:
     inverse_rht: mapped back through the transform of cfg (pass False for a
     cache written without it)."""
     kinds, lds = [], []
+    shape = (slots.numel(), cache.heads * cache.dim)
     for t, name in ((k_out, "k_out"), (v_out, "v_out")):
         if t is None:
             lds.append(0)
             continue
         kind, rows, cols, ld = _rows(t, name)
-        if (rows, cols) != (slots.numel(), cache.heads * cache.dim):
+        if (rows, cols) != shape:
             raise ValueError(f"{name} must be [tokens, heads * dim] with one row a slot")
         kinds.append(kind)
         lds.append(ld)
-    if len(set(kinds)) > 1:
+    if len(kinds) == 2 and kinds[0] != kinds[1]:
         raise TypeError("k_out and v_out must have one type")
-    with _on_device_of(stream, _int64(slots, "slots"), k_out, v_out, *cache.tensors) as s:
-        check("ufp4_cache_read",
-              lib.ufp4_cache_read(ctypes.byref(cfg), ctypes.byref(cache.c()), _ptr(slots), slots.numel(),
-                                  int(bool(inverse_rht)), _ptr(k_out), lds[0], _ptr(v_out), lds[1],
-                                  kinds[0] if kinds else TYPE_BF16, s))
+    _call("ufp4_cache_read", _one_device(_int64(slots, "slots"), k_out, v_out, cache.k_codes), stream, cfg, cache.c(),
+          slots.data_ptr(), slots.numel(), 1 if inverse_rht else 0, _ptr(k_out), lds[0], _ptr(v_out), lds[1],
+          kinds[0] if kinds else TYPE_BF16)
 
 
 class AttentionWorkspace(_Scratch):
@@ -758,14 +768,12 @@ def ufp4_tree_attention(cfg: ufp4_config, cache: QCache, q: torch.Tensor, q_offs
         raise ValueError("page_table must have one line a sequence")
     if mask is not None and mask.numel() != rows:
         raise ValueError("mask must have one entry a row of q")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (rows, heads) or not lse.is_contiguous()):
+    if lse is not None and (lse.dtype != torch.float32 or lse.shape != (rows, heads) or not lse.is_contiguous()):
         raise TypeError("lse must be a contiguous float32 tensor [rows, q_heads]")
     scale = cache.dim ** -0.5 if softmax_scale is None else float(softmax_scale)
-    with _on_device_of(stream, q, out, _int64(q_offsets, "q_offsets"), _int32(lengths, "lengths"),
-                       _int32(page_table, "page_table"), None if mask is None else _int64(mask, "mask"), lse, ws.buf,
-                       *cache.tensors) as s:
-        check("ufp4_tree_attention",
-              lib.ufp4_tree_attention(ctypes.byref(cfg), ctypes.byref(cache.c()), _ptr(q), ldq, heads, _ptr(q_offsets),
-                                      sequences, rows, int(max_draft), _ptr(lengths), _ptr(page_table),
-                                      page_table.shape[1], _ptr(mask), scale, _ptr(out), ldo, _ptr(lse), ws.ptr,
-                                      ws.nbytes, s))
+    device = _one_device(q, out, _int64(q_offsets, "q_offsets"), _int32(lengths, "lengths"),
+                         _int32(page_table, "page_table"), None if mask is None else _int64(mask, "mask"), lse, ws.buf,
+                         cache.k_codes)
+    _call("ufp4_tree_attention", device, stream, cfg, cache.c(), q.data_ptr(), ldq, heads, q_offsets.data_ptr(), sequences,
+          rows, int(max_draft), lengths.data_ptr(), page_table.data_ptr(), page_table.shape[1], _ptr(mask), scale,
+          out.data_ptr(), ldo, _ptr(lse), ws.ptr, ws.nbytes)

@@ -38,7 +38,7 @@ def make(env, pages, P, H, D, grid, scaled=True, fill=0xA7):
         ka = va = np.full(H, ref.QMAX[grid] * 448.0, np.float32)
         ks = vs = None
     c = F.alloc_cache(pages, P, H, D, ks, vs)
-    for t in c.tensors[:4]:
+    for t in c._tensors[:4]:
         t.fill_(fill)
     return c, ka, va
 
@@ -61,7 +61,7 @@ def check_written(env, cfg, c, k, v, slots, ka, va, fill=0xA7):
     torch, F, orc = env
     H, D, P = c.heads, c.dim, c.page_tokens
     ocfg = orc.config(grid=cfg.grid, rht=cfg.rht, rht_seed=cfg.rht_seed)
-    want = [np.full(t.shape, fill, np.uint8) for t in c.tensors[:4]]
+    want = [np.full(t.shape, fill, np.uint8) for t in c._tensors[:4]]
     s = slots.cpu().numpy()
     live = np.nonzero((s >= 0) & (s < c.pages * P))[0]
     page, at = s[live] // P, s[live] % P
@@ -74,7 +74,7 @@ def check_written(env, cfg, c, k, v, slots, ka, va, fill=0xA7):
             else:
                 codes[page, h, at] = oc[live]
                 scales[page, h, at] = os[live]
-    for t, w in zip(c.tensors[:4], want):
+    for t, w in zip(c._tensors[:4], want):
         assert np.array_equal(t.cpu().numpy(), w)
 
 
