@@ -55,7 +55,8 @@ struct CacheParams {
   CacheView c;
   int32_t grid, rht;  // rht: transform (append), inverse transform (read)
   RhtSigns sg;
-  float d[16];  // signs of the inverse transform
+  uint32_t signs;  // of the inverse transform, bit j set: -1
+  FastDiv pieces;  // division by the pieces (of one lane) of a token's head
   int64_t tokens;
   const int64_t* slots;
   const uint16_t* k;

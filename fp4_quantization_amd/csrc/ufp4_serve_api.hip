@@ -10,6 +10,7 @@ namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 25;
 constexpr int64_t kMaxTokens = (int64_t)1 << 21;  // of a product: a launch has 2^16 blocks of 64 in y
+constexpr int64_t kMaxLd = 0x7FFFFFFF;  // of a cache call's rows
 constexpr int64_t kMaxRows = (int64_t)1 << 28;
 constexpr int32_t kMaxSequences = 65535;  // of a launch in y
 constexpr int64_t kMaxSlots64 = (int64_t)1 << 40;
@@ -19,15 +20,11 @@ bool type_ok(int32_t t) { return t == UFP4_BF16 || t == UFP4_F32; }
 size_t type_size(int32_t t) { return t == UFP4_F32 ? 4 : 2; }
 int done(hipError_t e) { return e == hipSuccess ? UFP4_OK : UFP4_ERR_HIP; }
 
-void signs_of(const ufp4_config* cfg, RhtSigns& sg, float* d) {
-  QuantParams tmp;
-  fill_rht_signs(cfg->rht_seed, tmp);
-  sg = tmp.sg;
-  if (!d) return;
-  const uint32_t mask = rht_sign_mask(cfg->rht_seed);
-  for (int j = 0; j < 16; ++j) d[j] = ((mask >> j) & 1u) ? -1.0f : 1.0f;
+RhtSigns signs_of(const ufp4_config* cfg) {
+  QuantParams q;
+  fill_rht_signs(cfg->rht_seed, q);
+  return q.sg;
 }
-
 int check_matvec(const ufp4_config* cfg, int64_t tokens, int64_t N, int64_t K) {
   if (!cfg || cfg->grid < 0 || cfg->grid > 3 || (cfg->scaling != UFP4_SCALE_NV16 && cfg->scaling != UFP4_SCALE_MX32))
     return UFP4_ERR_INVALID_ARGUMENT;
@@ -116,7 +113,7 @@ int ufp4_matvec(const ufp4_config* cfg, const void* x, int32_t x_type, int64_t t
   p.grid = cfg->grid;
   p.mx = mx;
   p.rht = cfg->rht != 0;
-  signs_of(cfg, p.sg, nullptr);
+  p.sg = signs_of(cfg);
   p.y = y;
   if (need) {
     p.xp = static_cast<uint16_t*>(ws);
@@ -134,13 +131,14 @@ int ufp4_cache_append(const ufp4_config* cfg, const ufp4_cache* cache, const uin
   if (rc) return rc;
   const int64_t width = (int64_t)cache->heads * cache->dim;
   if (tokens < 0 || ldk < width || ldv < width) return UFP4_ERR_INVALID_ARGUMENT;
-  if (tokens >= kMaxRows) return UFP4_ERR_SHAPE;
+  if (tokens >= kMaxRows || ldk > kMaxLd || ldv > kMaxLd) return UFP4_ERR_SHAPE;
   if (tokens == 0) return UFP4_OK;
   if (!k || !v || !slots) return UFP4_ERR_INVALID_ARGUMENT;
   if (!aligned(k, 2) || !aligned(v, 2) || !aligned(slots, 8)) return UFP4_ERR_ALIGNMENT;
   p.grid = cfg->grid;
   p.rht = cfg->rht != 0;
-  signs_of(cfg, p.sg, p.d);
+  p.sg = signs_of(cfg);
+  p.signs = rht_sign_mask(cfg->rht_seed);
   p.tokens = tokens;
   p.slots = slots;
   p.k = k;
@@ -161,14 +159,15 @@ int ufp4_cache_read(const ufp4_config* cfg, const ufp4_cache* cache, const int64
   const int64_t width = (int64_t)cache->heads * cache->dim;
   if (!type_ok(out_type) || tokens < 0 || (k_out && ldk < width) || (v_out && ldv < width))
     return UFP4_ERR_INVALID_ARGUMENT;
-  if (tokens >= kMaxRows) return UFP4_ERR_SHAPE;
+  if (tokens >= kMaxRows || (k_out && ldk > kMaxLd) || (v_out && ldv > kMaxLd)) return UFP4_ERR_SHAPE;
   if (tokens == 0 || (!k_out && !v_out)) return UFP4_OK;
   if (!slots) return UFP4_ERR_INVALID_ARGUMENT;
   if (!aligned(k_out, type_size(out_type)) || !aligned(v_out, type_size(out_type)) || !aligned(slots, 8))
     return UFP4_ERR_ALIGNMENT;
   p.grid = cfg->grid;
   p.rht = inverse_rht != 0;
-  signs_of(cfg, p.sg, p.d);
+  p.sg = signs_of(cfg);
+  p.signs = rht_sign_mask(cfg->rht_seed);
   p.tokens = tokens;
   p.slots = slots;
   p.k_out = k_out;

@@ -548,7 +548,8 @@ typedef struct {
  * under the head's S_t, rounded to nearest even.  A slot outside [0, pages *
  * page_tokens) drops its token.  Slots of one call that are written must
  * differ (what a slot named twice holds afterwards is not defined).
- * cfg: NV16 and RTNE only (UFP4_ERR_INVALID_ARGUMENT); grid, rht, rht_seed. */
+ * cfg: NV16 and RTNE only (UFP4_ERR_INVALID_ARGUMENT); grid, rht, rht_seed.
+ * tokens < 2^28, leading dimensions < 2^31 (UFP4_ERR_SHAPE), here and below. */
 int ufp4_cache_append(const ufp4_config* cfg, const ufp4_cache* cache, const uint16_t* k, int64_t ldk,
                       const uint16_t* v, int64_t ldv, int64_t tokens, const int64_t* slots, ufp4_stream_t stream);
 
