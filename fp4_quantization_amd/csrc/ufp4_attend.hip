@@ -34,7 +34,7 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kAtWaves = 4, kAtThreads = 64 * kAtWaves;
 // Waves a SIMD holds of the kernel, which gives a wave 256 registers or 512.
-constexpr int attend_waves(int dt, int r) { return dt > 128 && r > 1 ? 1 : 2; }
+constexpr int attend_waves(int dt, int r) { return dt > 128 ? (r > 1 ? 1 : 2) : (r > 1 ? 2 : 3); }
 constexpr int kStep = 32 * kAtWaves;  // tokens
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
 
@@ -339,37 +339,43 @@ template <int GRID>
 constexpr float unshift() { return (float)(1 << kExpandShift<GRID>); }
 
 // ---------------------------------------------------------------- the kernel
-// What a wave reads of a tile of 32 tokens: this lane's parts of two keys (row r
-// of the first product's two tiles of 16) and of the values.
+// What a lane loads of a tile of 32 tokens: its parts of two keys (row r of the first
+// product's two tiles of 16), and, 16 (or 4, 8) bytes a lane as they lie in memory,
+// the scales of the keys and the values' codes and scales.  These three go through
+// LDS, a wave its own, where lanes find the bytes they need: loading those from
+// memory took twice as many, smaller loads.
 template <int DT>
 struct Tile {
   static constexpr int kWords = DT == 64 ? 2 : 4, kParts = (DT + 127) / 128, NT = DT / 32;
-  uint32_t kc[2][kParts][kWords], ks[2][kParts];
-  v32x2 vc[NT], vs[NT];
+  uint32_t kc[2][kParts][kWords];
+  v32x4 vc[NT / 2];
+  uint32_t ks[kParts], vs[kParts];
 };
-// A lane's byte offsets inside a tile of each array.  FULL: dim is DT; else parts of
-// a key past dim get an offset that is outside every tile, and read as zeros.
+template <int DT>
+struct TileLds {
+  v32x4 vc[DT];                                     // [pair of values][32 tokens], 16 DT bytes
+  uint32_t vs[64 * ((DT + 127) / 128)], ks[64 * ((DT + 127) / 128)];  // [block][32], [token][block]
+};
+// A lane's byte offsets of key parts inside a tile.  FULL: dim is DT; else parts past
+// dim get an offset that is outside every tile, and read as zeros.
 template <int DT, bool FULL>
 struct Offsets {
   static constexpr int kParts = Tile<DT>::kParts;
-  uint32_t kc[FULL ? 1 : kParts], ks[FULL ? 1 : kParts], vc, vs;
+  uint32_t kc[FULL ? 1 : kParts];
   __device__ __forceinline__ Offsets(int dim, int g, int r) {
     const int tok = 8 * (r >> 2) + (r & 3);
 #pragma unroll
     for (int c = 0; c < (FULL ? 1 : kParts); ++c) {
       const int d = g * (DT / 4) + 32 * c;
-      const bool in = FULL || d < dim;
-      kc[c] = in ? (uint32_t)(tok * (FULL ? DT : dim) + d) / 2 : 0x80000000u;
-      ks[c] = in ? (uint32_t)(tok * (FULL ? DT : dim) + d) / 16 : 0x80000000u;
+      kc[c] = FULL || d < dim ? (uint32_t)(tok * (FULL ? DT : dim) + d) / 2 : 0x80000000u;
     }
-    vc = (uint32_t)(r * 32 + 8 * g);
-    vs = (uint32_t)((r >> 3) * 32 + 8 * g);
   }
 };
 // The tile whose first token has index `at` in its cache (page, head, token); !ok:
 // nothing is read.
 template <int DT, bool FULL>
-__device__ __forceinline__ void load_tile(const AttendParams& p, int64_t at, bool ok, const Offsets<DT, FULL>& off, Tile<DT>& x) {
+__device__ __forceinline__ void load_tile(const AttendParams& p, int64_t at, bool ok, int lane, const Offsets<DT, FULL>& off,
+                                          Tile<DT>& x) {
   const int half = FULL ? DT / 2 : p.c.dim / 2, blocks = FULL ? DT / 16 : p.c.dim / 16;
   const int bytes = ok ? kCacheTile * half : 0, sbytes = ok ? kCacheTile * blocks : 0;
   // word 3: 32-bit data, raw addressing
@@ -381,25 +387,40 @@ __device__ __forceinline__ void load_tile(const AttendParams& p, int64_t at, boo
   for (int u = 0; u < 2; ++u)
 #pragma unroll
     for (int c = 0; c < Tile<DT>::kParts; ++c) {
-      const int ko = (int)(FULL ? off.kc[0] + 16 * c + 4 * u * half : off.kc[FULL ? 0 : c]), ks0 = FULL ? 0 : 4 * u * half;
-      const int so = (int)(FULL ? off.ks[0] + 2 * c + 4 * u * blocks : off.ks[FULL ? 0 : c]), ss0 = FULL ? 0 : 4 * u * blocks;
+      const int ko = (int)(FULL ? off.kc[0] + 16 * c + 4 * u * half : off.kc[FULL ? 0 : c]), k0 = FULL ? 0 : 4 * u * half;
       if constexpr (DT == 64) {
-        const v32x2 w = __builtin_bit_cast(v32x2, __builtin_amdgcn_raw_buffer_load_b64(kc, ko, ks0, 0));
+        const v32x2 w = __builtin_bit_cast(v32x2, __builtin_amdgcn_raw_buffer_load_b64(kc, ko, k0, 0));
         x.kc[u][c][0] = w.x;
         x.kc[u][c][1] = w.y;
-        x.ks[u][c] = __builtin_amdgcn_raw_buffer_load_b8(ks, so, ss0, 0);
       } else {
-        const v32x4 w = __builtin_bit_cast(v32x4, __builtin_amdgcn_raw_buffer_load_b128(kc, ko, ks0, 0));
+        const v32x4 w = __builtin_bit_cast(v32x4, __builtin_amdgcn_raw_buffer_load_b128(kc, ko, k0, 0));
 #pragma unroll
         for (int j = 0; j < 4; ++j) x.kc[u][c][j] = w[j];
-        x.ks[u][c] = __builtin_amdgcn_raw_buffer_load_b16(ks, so, ss0, 0);
       }
     }
 #pragma unroll
-  for (int t = 0; t < DT / 32; ++t) {
-    x.vc[t] = __builtin_bit_cast(v32x2, __builtin_amdgcn_raw_buffer_load_b64(vc, (int)off.vc + 512 * t, 0, 0));
-    x.vs[t] = __builtin_bit_cast(v32x2, __builtin_amdgcn_raw_buffer_load_b64(vs, (int)off.vs + 64 * t, 0, 0));
+  for (int t = 0; t < DT / 64; ++t) x.vc[t] = __builtin_bit_cast(v32x4, __builtin_amdgcn_raw_buffer_load_b128(vc, 16 * lane + 1024 * t, 0, 0));
+#pragma unroll
+  for (int c = 0; c < Tile<DT>::kParts; ++c) {
+    x.ks[c] = __builtin_amdgcn_raw_buffer_load_b32(ks, 4 * lane + 256 * c, 0, 0);
+    x.vs[c] = __builtin_amdgcn_raw_buffer_load_b32(vs, 4 * lane + 256 * c, 0, 0);
   }
+}
+// Through a wave's LDS: what the wave writes here, it reads itself, in order; the
+// barriers are the compiler's alone.
+template <int DT>
+__device__ __forceinline__ void stage_tile(const Tile<DT>& x, int lane, TileLds<DT>& to) {
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+#pragma unroll
+  for (int t = 0; t < DT / 64; ++t) to.vc[lane + 64 * t] = x.vc[t];
+#pragma unroll
+  for (int c = 0; c < Tile<DT>::kParts; ++c) {
+    to.ks[lane + 64 * c] = x.ks[c];
+    to.vs[lane + 64 * c] = x.vs[c];
+  }
+  __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+  __builtin_amdgcn_wave_barrier();
 }
 
 template <int GRID, int DT, int R, int PARTS, bool FULL>
@@ -408,13 +429,14 @@ __global__ __launch_bounds__(kAtThreads, attend_waves(DT, R)) void ufp4_attend_k
   constexpr int kPitch = DT + 4;
   // fragments of q that fit 32 registers stay in them, else they are read from LDS
   // for every two tiles of 16 tokens
-  constexpr bool kInLds = R * NT >= 8;
+  constexpr bool kInLds = R * NT >= 4;
   __shared__ Signs S;
   __shared__ f16x8 ql[R][PARTS][NT][64];
   __shared__ int qshift[ROWS];
   __shared__ int64_t sh[kAtWaves + 2];
   __shared__ float ml[kAtWaves][2][ROWS];
   __shared__ float join[2][ROWS][kPitch];
+  __shared__ TileLds<DT> staged[kAtWaves];
   const int tid = threadIdx.x, wave = uniform(tid >> 6), lane = tid & 63, g = lane >> 4, r = lane & 15;
   if (tid < 8) {
     const uint32_t m = p.signs;
@@ -459,22 +481,33 @@ __global__ __launch_bounds__(kAtThreads, attend_waves(DT, R)) void ufp4_attend_k
       for (int t = 0; t < 2 * NT; ++t) o[i][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
     }
 
-    // this wave's tiles: the page of the one after the next is read, the next one
-    // is on its way, this one is computed
+    const int blocks = FULL ? DT / 16 : p.c.dim / 16;
+    // this wave's tiles: the next one is on its way while one is computed.  Their
+    // pages are held 64 steps at a time, one a lane: a scalar load for each tile
+    // would be waited for with every access to LDS, since the two share a counter
+    // that scalar loads leave in any order.
+    int pages_from = step0, pages = -1;
+    auto load_pages = [&]() {
+      const int t0 = (pages_from + lane) * kStep + 32 * wave;
+      pages = pages_from + lane < step1 && t0 < s.len ? table[p.c.page.div((uint32_t)t0)] : -1;
+    };
+    load_pages();
     auto page_of = [&](int step) {
-      const int t0 = step * kStep + 32 * wave;
-      return step < step1 && t0 < s.len ? uniform(table[p.c.page.div((uint32_t)t0)]) : -1;
+      if (step - pages_from >= 64) {
+        pages_from = step;
+        load_pages();
+      }
+      return __builtin_amdgcn_readlane(pages, step - pages_from);
     };
     auto fetch = [&](int step, int page, Tile<DT>& x) {
       const bool ok = page >= 0 && page < p.c.pages;
       const int t0 = step * kStep + 32 * wave;
       const int in_page = t0 - (int)p.c.page.div((uint32_t)t0) * p.c.page_tokens;
-      load_tile<DT, FULL>(p, ok ? ((int64_t)page * p.c.heads + h) * p.c.page_tokens + in_page : 0, ok, off, x);
+      load_tile<DT, FULL>(p, ok ? ((int64_t)page * p.c.heads + h) * p.c.page_tokens + in_page : 0, ok, lane, off, x);
       return ok;
     };
     Tile<DT> next;
     bool next_ok = fetch(step0, page_of(step0), next);
-    int page = page_of(step0 + 1);
 
     // rows of q, by one wave for each 16
     if (wave < R) {
@@ -507,17 +540,27 @@ __global__ __launch_bounds__(kAtThreads, attend_waves(DT, R)) void ufp4_attend_k
     for (int step = step0; step < step1; ++step) {
       const Tile<DT> x = next;
       const bool ok = next_ok;
-      next_ok = fetch(step + 1, page, next);
-      page = page_of(step + 2);
+      next_ok = fetch(step + 1, page_of(step + 1), next);
       if (!ok) continue;
       const int t0 = step * kStep + 32 * wave;
+      stage_tile<DT>(x, lane, staged[wave]);
+      const uint8_t* ks = reinterpret_cast<const uint8_t*>(staged[wave].ks) + (8 * (r >> 2) + (r & 3)) * blocks + g * (DT / 64);
+      const uint8_t* vc = reinterpret_cast<const uint8_t*>(staged[wave].vc) + r * 32 + 8 * g;
+      const uint8_t* vs = reinterpret_cast<const uint8_t*>(staged[wave].vs) + (r >> 3) * 32 + 8 * g;
       // ---- logits
       f32x4 a[R][2];
 #pragma unroll
       for (int i = 0; i < R; ++i) a[i][0] = a[i][1] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
       for (int c = 0; c < Tile<DT>::kParts; ++c) {
-        const f16x2 ds[2] = {expand_scales<GRID>(x.ks[0][c] & 0x7F7Fu), expand_scales<GRID>(x.ks[1][c] & 0x7F7Fu)};
+        f16x2 ds[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* from = ks + 4 * u * blocks + 2 * c;
+          uint32_t two = DT == 64 ? (uint32_t)*from : (uint32_t)*reinterpret_cast<const uint16_t*>(from);
+          if (!FULL && g * (DT / 4) + 32 * c >= p.c.dim) two = 0;
+          ds[u] = expand_scales<GRID>(two & 0x7F7Fu);
+        }
 #pragma unroll
         for (int j = 0; j < Tile<DT>::kWords; ++j) {
           f16x8 kf[2];
@@ -587,12 +630,13 @@ __global__ __launch_bounds__(kAtThreads, attend_waves(DT, R)) void ufp4_attend_k
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         if (!FULL && 32 * t >= p.c.dim) break;
+        const v32x2 codes = *reinterpret_cast<const v32x2*>(vc + 512 * t), scales = *reinterpret_cast<const v32x2*>(vs + 64 * t);
         f16x2 s01, s23, s45, s67;
-        scales_of<GRID>(x.vs[t].x & keep0, s01, s23);
-        scales_of<GRID>(x.vs[t].y & keep1, s45, s67);
+        scales_of<GRID>(scales.x & keep0, s01, s23);
+        scales_of<GRID>(scales.y & keep1, s45, s67);
         uint32_t v0[4], v1[4];
-        expand_tokens<GRID>(x.vc[t].x, s01, s23, v0, v1);
-        expand_tokens<GRID>(x.vc[t].y, s45, s67, v0 + 2, v1 + 2);
+        expand_tokens<GRID>(codes.x, s01, s23, v0, v1);
+        expand_tokens<GRID>(codes.y, s45, s67, v0 + 2, v1 + 2);
         const f16x8 even = __builtin_bit_cast(f16x8, g32x4{v0[0], v0[1], v0[2], v0[3]});
         const f16x8 odd = __builtin_bit_cast(f16x8, g32x4{v1[0], v1[1], v1[2], v1[3]});
 #pragma unroll
@@ -774,7 +818,7 @@ int attend_rows(int32_t dim, int32_t group, int32_t max_draft) { return (int64_t
 
 // Runs of a launch: the workgroups that 256 compute units hold at once (one where
 // a wave takes more than half of the registers).
-int32_t attend_runs(int32_t dim, int32_t rows) { return dim > 128 && rows > 16 ? 256 : 512; }
+int32_t attend_runs(int32_t dim, int32_t rows) { return 256 * attend_waves(dim, rows / 16); }
 
 hipError_t launch_attend(const AttendParams& p, hipStream_t s) {
   switch (p.grid) {
