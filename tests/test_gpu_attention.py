@@ -127,3 +127,104 @@ CASES = [
 def test_values(env, lengths, drafts, H, G, D, P, grid, rht, is_tree):
     cfg, c, table = build(env, lengths, H, D, P, grid, rht)
     compare(env, cfg, c, table, lengths, drafts, G, mask=tree(env[0], drafts, 3) if is_tree else None)
+
+
+@pytest.mark.parametrize("rht", [0, 1])
+def test_rows_that_see_nothing(env, rht):
+    """Masks that leave a row (or all of a sequence) empty, histories of no token,
+    more drafted tokens than the cache holds, lengths outside the table."""
+    torch, F = env
+    lengths, drafts = [3, 0, 40, 2, 33], [3, 2, 4, 5, 2]
+    cfg, c, table = build(env, lengths, 2, 64, 32, E1M2, rht)
+    mask = tree(torch, drafts, 1)
+    mask[0] = 0          # no history, sees nothing
+    mask[2] = 0b010      # one other token alone
+    mask[5] = 0          # sees its history
+    mask[9:14] = -1      # bits of tokens that do not exist
+    compare(env, cfg, c, table, lengths, drafts, 3, mask=mask)
+    compare(env, cfg, c, table, lengths, drafts, 3)
+    compare(env, cfg, c, table, [-5, 1 << 30, 40, 0, 33], drafts, 3)
+
+
+def test_rows_left_out(env):
+    """Drafted tokens past max_draft, sequences whose rows lie outside q."""
+    torch, F = env
+    lengths, drafts = [50, 70, 20], [6, 3, 9]
+    cfg, c, table = build(env, lengths, 1, 96, 32, E2M1, 1)
+    compare(env, cfg, c, table, lengths, drafts, 2, max_draft=4)
+    compare(env, cfg, c, table, lengths, drafts, 2, max_draft=9, offsets=[0, 6, 4, 13])
+    compare(env, cfg, c, table, lengths, drafts, 2, max_draft=9, offsets=[-2, 4, 7, 16])
+
+
+def test_pages_outside_the_cache(env):
+    torch, F = env
+    lengths, drafts = [300, 64], [2, 1]
+    cfg, c, table = build(env, lengths, 2, 128, 32, INT4, 1)
+    table[0, 1], table[0, 4], table[1, 0] = -1, c.pages, 1 << 30
+    compare(env, cfg, c, table, lengths, drafts, 2)
+    table[1, 1] = -(1 << 31)  # nothing left of the second sequence
+    compare(env, cfg, c, table, lengths, drafts, 2)
+
+
+@pytest.mark.parametrize("spread,scale", [(1.5, 0.0), (30.0, 1.0), (1e-30, 0.1), (1e4, 1e-4), (1.5, -0.2)])
+def test_logits_of_all_sizes(env, spread, scale):
+    cfg, c, table = build(env, [260, 31], 2, 64, 32, E1M2, 1)
+    compare(env, cfg, c, table, [260, 31], [3, 1], 2, scale=scale, spread=spread)
+
+
+@pytest.mark.parametrize("scaled", [True, False])
+def test_head_scales(env, scaled):
+    """No tensor scales, and entries that are not positive finite numbers: 1."""
+    torch, F = env
+    cfg, c, table = build(env, [100], 3, 64, 32, E1M2, 0, scaled=scaled)
+    if scaled:
+        c.k_scale[0], c.k_scale[1], c.v_scale[2] = 0.0, float("nan"), float("inf")
+    compare(env, cfg, c, table, [100], [1], 1, scale=0.01)
+
+
+def test_a_lost_row_stays_alone(env):
+    """NaN and infinities in one query row: the others are bit for bit what they were."""
+    torch, F = env
+    cfg, c, table = build(env, [200, 70], 2, 128, 32, E1M2, 1)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q = torch.randn(9, 4 * 128, device="cuda", generator=g).bfloat16()
+    off, lens = torch.tensor([0, 6, 9], device="cuda"), torch.tensor([200, 70], dtype=torch.int32, device="cuda")
+    ws = F.AttentionWorkspace(c, 4, 2, 6)
+    outs = []
+    for bad in (None, float("nan"), float("inf")):
+        x = q.clone()
+        if bad is not None:
+            x[4, 130] = bad
+        o = torch.empty_like(x)
+        F.ufp4_tree_attention(cfg, c, x, off, lens, table, 6, o, ws)
+        outs.append(o.view(9, 4, 128))
+    for o in outs[1:]:
+        assert bool(torch.isnan(o[4, 1].float()).all())
+        o[4, 1] = outs[0][4, 1]
+        assert torch.equal(o, outs[0])
+
+
+def test_many_sequences_and_long_runs(env):
+    """More sequences than a workgroup has threads, and runs of more steps than a
+    wave holds pages of: the same rows as in calls of a few sequences."""
+    torch, F = env
+    g = torch.Generator(device="cuda").manual_seed(2)
+    for B, H, lens in ((700, 1, None), (26, 32, 16384)):
+        lengths = [lens or int(n) for n in torch.randint(0, 300, (B,), generator=torch.Generator().manual_seed(1))]
+        cfg, c, table = build(env, lengths, H, 32, 64, E1M2, 1, garbage=False)
+        q = torch.randn(B, H * 32, device="cuda", generator=g).bfloat16()
+        dev = torch.tensor(lengths, dtype=torch.int32, device="cuda")
+
+        def run(rows):
+            n = len(rows)
+            o = torch.empty(n, H * 32, dtype=torch.bfloat16, device="cuda")
+            F.ufp4_tree_attention(cfg, c, q[rows].contiguous(), torch.arange(n + 1, device="cuda"), dev[rows].contiguous(),
+                                  table[rows].contiguous(), 1, o, F.AttentionWorkspace(c, H, n, 1))
+            return o
+
+        whole = run(list(range(B)))
+        for rows in ([0, 1], [B // 2], [B - 2, B - 1]):
+            few = run(rows)
+            # sums of other lengths: a rounding of bf16 and fp16's of the weights apart
+            err = (few.float() - whole[rows].float()).abs()
+            assert bool((err <= 2.0 ** -7 * few.float().abs() + 2.0 ** -10 * few.float().abs().amax(1, keepdim=True)).all())

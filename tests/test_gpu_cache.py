@@ -132,3 +132,60 @@ def test_append_and_read(env, T, pages, P, H, D, grid, rht, scaled, special, ord
         assert torch.equal(one, want[1].to(kind))
         F.ufp4_cache_read(cfg, c, slots, one, None, bool(rht))
         assert torch.equal(one, want[0].to(kind))
+
+
+def test_past_32_bits(env):
+    """A cache of more than 4 GiB of codes: slots at its end, read by attention too."""
+    torch, F, orc = env
+    H, D, P = 8, 256, 256
+    pages = (1 << 32) // (P * H * D // 2) + 9
+    cfg = F.config(rht=1, rht_seed=4)
+    c = F.alloc_cache(pages, P, H, D)
+    assert c.k_codes.numel() > 1 << 32
+    T = 70
+    slots = torch.arange(T, device="cuda") + (pages - 1) * P + 11
+    k, v = (inputs(torch, T, H * D, s, False) for s in (3, 4))
+    F.ufp4_cache_append(cfg, c, k, v, slots)
+    small = F.alloc_cache(2, P, H, D)
+    near = torch.arange(T, device="cuda") + 11
+    F.ufp4_cache_append(cfg, small, k, v, near)
+    outs = []
+    for cache, s, page in ((c, slots, pages - 1), (small, near, 0)):
+        a, b = (torch.empty(T, H * D, device="cuda") for _ in range(2))
+        F.ufp4_cache_read(cfg, cache, s, a, b)
+        o = torch.empty(1, H * D, dtype=torch.bfloat16, device="cuda")
+        # the first 11 slots of the page: written too
+        F.ufp4_cache_append(cfg, cache, k[:11], v[:11], torch.arange(11, device="cuda") + page * P)
+        F.ufp4_tree_attention(cfg, cache, k[:1], torch.tensor([0, 1], device="cuda"), torch.tensor([81], dtype=torch.int32, device="cuda"),
+                              torch.tensor([[page]], dtype=torch.int32, device="cuda"), 1, o, F.AttentionWorkspace(cache, H, 1, 1))
+        outs.append((a, b, o))
+    assert all(torch.equal(x, y) for x, y in zip(*outs))
+
+
+@pytest.mark.parametrize("ts", [0.0, -1.0, float("nan"), float("inf")])
+def test_tensor_scales_that_are_none(env, ts):
+    torch, F, orc = env
+    cfg = F.config(rht=0)
+    k = inputs(torch, 40, 64, 1, False)
+    slots = torch.arange(40, device="cuda")
+    got = []
+    for scale in (None, torch.full((2,), ts, device="cuda")):
+        c = F.alloc_cache(2, 32, 2, 32, scale, scale)
+        F.ufp4_cache_append(cfg, c, k, k, slots)
+        a = torch.empty(40, 64, device="cuda")
+        F.ufp4_cache_read(cfg, c, slots, a, None, False)
+        got.append(a)
+    assert torch.equal(*got)
+
+
+def test_a_slot_read_twice(env):
+    torch, F, orc = env
+    cfg = F.config(rht=1)
+    k = inputs(torch, 5, 32, 1, False)
+    c = F.alloc_cache(1, 32, 1, 32)
+    F.ufp4_cache_append(cfg, c, k, k, torch.arange(5, device="cuda"))
+    a = torch.empty(9, 32, device="cuda")
+    F.ufp4_cache_read(cfg, c, torch.tensor([1, 1, 4, 1, 0, 4, 4, 2, 1], device="cuda"), None, a)
+    b = torch.empty(5, 32, device="cuda")
+    F.ufp4_cache_read(cfg, c, torch.arange(5, device="cuda"), None, b)
+    assert torch.equal(a, b[torch.tensor([1, 1, 4, 1, 0, 4, 4, 2, 1], device="cuda")])

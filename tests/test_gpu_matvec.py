@@ -75,7 +75,7 @@ CASES = [
     (1, 40, 256, E1M2, MX32, 1, "bf16", "f32"), (1, 64, 4096, E2M1, MX32, 0, "bf16", "bf16"),
     (3, 65, 96, INT4, MX32, 0, "bf16", "f32"), (7, 129, 1056, E2M1, MX32, 1, "f32", "f32"),
     (33, 47, 2080, INT4, MX32, 1, "f32", "f32"), (70, 30, 160, E2M1C, MX32, 1, "bf16", "bf16"),
-    (2, 16, 32768, E1M2, MX32, 0, "f32", "f32"), (4, 19, 65536, E2M1, NV16, 1, "bf16", "f32"),
+    (2, 16, 32768, E1M2, MX32, 0, "f32", "f32"), (4, 20, 11264, E1M2, NV16, 1, "bf16", "bf16"), (4, 19, 65536, E2M1, NV16, 1, "bf16", "f32"),
 ]
 
 
@@ -125,3 +125,77 @@ def test_whole_numbers(env, T, scaling, grid, rht):
     if rht:
         xd = ref.along(xd, ref.hadamard(F.ufp4_rht_signs(5)))
     assert torch.equal(y.double(), xd @ ref.values(q.codes, q.scales, grid, scaling == MX32).T)
+
+
+def test_empty(env):
+    torch, F = env
+    cfg = F.config()
+    y = torch.full((20, 16), -7.0, device="cuda")
+    for T in (1, 20):  # K of 0: zeros
+        q = F.QTensor(*(torch.empty(s, dtype=torch.uint8, device="cuda") for s in ((16, 0), (16, 0))), torch.ones(1, device="cuda"))
+        F.ufp4_matvec(cfg, torch.empty(T, 0, device="cuda"), q, y[:T], F.MatvecWorkspace(T, 16, 0, cfg))
+        assert bool((y[:T] == 0).all())
+    q = weights(env, 16, 64, cfg)
+    F.ufp4_matvec(cfg, torch.empty(0, 64, device="cuda"), q, y[:0])
+
+
+@pytest.mark.parametrize("T", [1, 4, 9, 40])
+@pytest.mark.parametrize("scaling", [NV16, MX32])
+@pytest.mark.parametrize("rht", [0, 1])
+def test_a_lost_token_stays_alone(env, T, scaling, rht):
+    """NaN or infinity in one token of x: NaN or infinities in its row, the other rows
+    bit for bit what they were."""
+    torch, F = env
+    N, K = 40, 544
+    cfg = F.config(scaling=scaling, rht=rht, rht_seed=3)
+    q, x = weights(env, N, K, cfg), rows(torch, T, K, torch.bfloat16)
+    ws = F.MatvecWorkspace(T, N, K, cfg)
+    outs = []
+    for bad in (None, float("nan"), float("inf")):
+        z = x.clone()
+        if bad is not None:
+            z[T // 2, 7] = bad
+        y = torch.empty(T, N, device="cuda")
+        F.ufp4_matvec(cfg, z, q, y, ws)
+        outs.append(y)
+    for y in outs[1:]:
+        assert not bool(torch.isfinite(y[T // 2]).any())
+        y[T // 2] = outs[0][T // 2]
+        assert torch.equal(y, outs[0])
+
+
+@pytest.mark.parametrize("size", [1e-38, 1e-20, 1e20, 3e38])
+@pytest.mark.parametrize("kind", ["bf16", "f32"])
+def test_tokens_of_all_sizes(env, size, kind):
+    """One token's magnitude does not matter to its relative error (a token near the
+    largest number: without the transform, whose fp32 sums may pass it)."""
+    torch, F = env
+    N, K = 30, 96
+    rht = int(size < 1e38)
+    cfg = F.config(rht=rht, rht_seed=3)
+    q = weights(env, N, K, cfg, spread=0.01)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = (torch.rand(2, K, device="cuda", generator=g) * 2 - 1) * size
+    x = x.to(torch.bfloat16) if kind == "bf16" else x
+    y = torch.empty(2, N, device="cuda")
+    F.ufp4_matvec(cfg, x, q, y)
+    want, bound = expected(env, cfg, x, q, torch.float32)
+    assert bool(((y.double() - want).abs() <= bound).all())
+
+
+def test_past_32_bits(env):
+    """Weights of more than 4 GiB of codes: rows at the end."""
+    torch, F = env
+    N, K = (1 << 19) + 37, 16640  # 4.06 GiB
+    cfg = F.config(rht=0)
+    q = F.alloc_layout(N, K, NV16)
+    q.codes.fill_(0)
+    q.scales.fill_(0x38)
+    q.tensor_scale.fill_(1.0)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    q.codes[-50:] = torch.randint(0, 256, (50, K // 2), device="cuda", generator=g, dtype=torch.uint8)
+    x = torch.randint(-2, 3, (2, K), device="cuda", generator=g).bfloat16()
+    y = torch.full((2, N), -7.0, device="cuda")
+    F.ufp4_matvec(cfg, x, q, y, F.MatvecWorkspace(2, N, K, cfg))
+    assert bool((y[:, :-50] == 0).all())
+    assert torch.equal(y[:, -50:].double(), x.double() @ ref.values(q.codes[-50:], q.scales[-50:], E1M2).T)
