@@ -192,17 +192,19 @@ __device__ __forceinline__ void dequantize(const CacheParams& p, v32x2 codes, ui
   for (int j = 0; j < N; ++j) v[j] = v[j] * ((mine >> j) & 1 ? -0.25f : 0.25f);
 }
 
+template <bool S>
 __device__ __forceinline__ void store_piece(uint16_t* out, const float v[16]) {
 #pragma unroll
   for (int h = 0; h < 16; h += 8)
-    store_16(out + h, v32x4{pack_bf16(v[h], v[h + 1]), pack_bf16(v[h + 2], v[h + 3]), pack_bf16(v[h + 4], v[h + 5]),
+    store_16<S>(out + h, v32x4{pack_bf16(v[h], v[h + 1]), pack_bf16(v[h + 2], v[h + 3]), pack_bf16(v[h + 4], v[h + 5]),
                             pack_bf16(v[h + 6], v[h + 7])});
 }
+template <bool S>
 __device__ __forceinline__ void store_piece(float* out, const float v[4]) {
-  store_16(out, v32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
+  store_16<S>(out, v32x4{__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3])});
 }
 
-template <int GRID, typename TO>
+template <int GRID, typename TO, bool S>
 __global__ __launch_bounds__(kCacheThreads) void ufp4_cache_read_kernel(CacheParams p) {
   constexpr int N = sizeof(TO) == 2 ? 16 : 4, kLanes = 16 / N;  // values a lane, lanes a block
   __shared__ int64_t place[kTok];
@@ -251,7 +253,7 @@ __global__ __launch_bounds__(kCacheThreads) void ufp4_cache_read_kernel(CachePar
 #pragma unroll
       for (int j = 0; j < N; ++j) v[j] = 0.0f;
       if (y.at >= 0) dequantize<GRID, N>(p, y.w, y.scale, kts, y.c % kLanes, v);
-      store_piece(k0 + (uint64_t)y.t * (uint32_t)p.ldk + N * y.c, v);
+      store_piece<S>(k0 + (uint64_t)y.t * (uint32_t)p.ldk + N * y.c, v);
     }
     if (p.v_out) {
 #pragma unroll
@@ -263,7 +265,7 @@ __global__ __launch_bounds__(kCacheThreads) void ufp4_cache_read_kernel(CachePar
         else w.x = *reinterpret_cast<const uint16_t*>(from);
         dequantize<GRID, N>(p, w, scales[y.t * kScalePitch + y.c / kLanes], vts, y.c % kLanes, v);
       }
-      store_piece(v0 + (uint64_t)y.t * (uint32_t)p.ldv + N * y.c, v);
+      store_piece<S>(v0 + (uint64_t)y.t * (uint32_t)p.ldv + N * y.c, v);
     }
   }
 }
@@ -274,8 +276,14 @@ template <int GRID>
 hipError_t launch_read(const CacheParams& p0, hipStream_t s) {
   CacheParams p = p0;
   p.pieces = fast_div((uint32_t)p.c.dim / (p.out_f32 ? 4 : 16));
-  if (p.out_f32) ufp4_cache_read_kernel<GRID, float><<<grid_of(p), kCacheThreads, 0, s>>>(p);
-  else ufp4_cache_read_kernel<GRID, uint16_t><<<grid_of(p), kCacheThreads, 0, s>>>(p);
+  const int64_t bytes = p.tokens * p.c.heads * p.c.dim * (p.out_f32 ? 4 : 2) * ((p.k_out != nullptr) + (p.v_out != nullptr));
+  // past the caches where most of it would not stay in them: 256 MB of results 60 us,
+  // through them 92
+  const bool past = bytes > kLastLevelCache / 2;
+  if (p.out_f32 && past) ufp4_cache_read_kernel<GRID, float, true><<<grid_of(p), kCacheThreads, 0, s>>>(p);
+  else if (p.out_f32) ufp4_cache_read_kernel<GRID, float, false><<<grid_of(p), kCacheThreads, 0, s>>>(p);
+  else if (past) ufp4_cache_read_kernel<GRID, uint16_t, true><<<grid_of(p), kCacheThreads, 0, s>>>(p);
+  else ufp4_cache_read_kernel<GRID, uint16_t, false><<<grid_of(p), kCacheThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 

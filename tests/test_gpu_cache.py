@@ -189,3 +189,23 @@ def test_a_slot_read_twice(env):
     b = torch.empty(5, 32, device="cuda")
     F.ufp4_cache_read(cfg, c, torch.arange(5, device="cuda"), None, b)
     assert torch.equal(a, b[torch.tensor([1, 1, 4, 1, 0, 4, 4, 2, 1], device="cuda")])
+
+
+@pytest.mark.parametrize("kind", ["float32", "bfloat16"])
+def test_large_reads(env, kind):
+    """Results larger than the caches are stored past them: the same values as in
+    calls of a few tokens."""
+    torch, F, orc = env
+    H, D, P, T = 8, 256, 64, 17000
+    kind = getattr(torch, kind)
+    cfg = F.config(rht=1, rht_seed=4)
+    c = F.alloc_cache(T // P + 1, P, H, D)
+    k = inputs(torch, T, H * D, 1, False)
+    slots = torch.arange(T, device="cuda")
+    F.ufp4_cache_append(cfg, c, k, k.flip(0).contiguous(), slots)
+    a, b = (torch.empty(T, H * D, dtype=kind, device="cuda") for _ in range(2))
+    F.ufp4_cache_read(cfg, c, slots, a, b)
+    for t in (0, 4099, T - 1000):
+        x, y = (torch.empty(1000, H * D, dtype=kind, device="cuda") for _ in range(2))
+        F.ufp4_cache_read(cfg, c, slots[t:t + 1000], x, y)
+        assert torch.equal(a[t:t + 1000], x) and torch.equal(b[t:t + 1000], y)
