@@ -99,7 +99,7 @@ __device__ Run run_of(const AttendParams& p, int64_t* sh) {
   for (int w = 0; w < kAtWaves; ++w) total += sh[w];
   Run r;
   r.each = (total + gridDim.x - 1) / gridDim.x;
-  if (r.each < p.min_steps) r.each = p.min_steps;
+  if (r.each < 1) r.each = 1;
   r.lo = blockIdx.x * r.each;
   r.hi = r.lo + r.each < total ? r.lo + r.each : total;
   r.b = -1;
@@ -731,19 +731,22 @@ __global__ __launch_bounds__(kAtThreads, attend_waves(DT, R)) void ufp4_attend_k
   if (tid == 0 && p.split) p.split[blockIdx.x] = split;
 }
 
-// Joins the partial results of the unit that begins in run blockIdx.x and ends in a
-// later one: 16 rows and 32 columns a workgroup, whose waves share the runs.
+// Joins the partial results of the unit that begins in a run and ends in a later one:
+// 16 rows and 32 columns a workgroup, whose waves share the runs.  The workgroups of
+// one run are neighbours, so that they lie on all XCDs: units of equal length begin
+// in every 2^n-th run, and with the runs as neighbours all work fell to one XCD.
 template <int GRID, int R>
 __global__ __launch_bounds__(kAtThreads) void ufp4_attend_join_kernel(AttendParams p) {
   constexpr int ROWS = 16 * R;
   __shared__ float ml[kAtWaves][2][64];
   __shared__ float part[kAtWaves][64][8 + 1];
-  const SplitUnit u = p.split[blockIdx.x];
+  const int slices = R * (p.c.dim / 32), slice = (int)blockIdx.x % slices, run = (int)blockIdx.x / slices;
+  const SplitUnit u = p.split[run];
   if (u.runs == 0) return;
   const int wave = uniform(threadIdx.x >> 6), lane = threadIdx.x & 63, g = lane >> 4, r = lane & 15;
-  const int i = blockIdx.y % R, col = blockIdx.y / R * 32;
+  const int i = slice % R, col = slice / R * 32;
   // run k of the unit is slot 1 of its first workgroup and slot 0 of the others
-  auto row_of = [&](int k) { return (2 * ((int64_t)blockIdx.x + k) + (k == 0)) * ROWS + 16 * i + r; };
+  auto row_of = [&](int k) { return (2 * ((int64_t)run + k) + (k == 0)) * ROWS + 16 * i + r; };
   float m = -__builtin_inff(), l = 0.0f;
   for (int k = wave; k < u.runs; k += kAtWaves) m = fmaxf(m, p.ml[row_of(k)].x);
   ml[wave][0][lane] = m;
@@ -786,13 +789,11 @@ __global__ __launch_bounds__(kAtThreads) void ufp4_attend_join_kernel(AttendPara
 }
 
 template <int GRID, int DT, int R>
-hipError_t launch_rows(const AttendParams& p0, hipStream_t s) {
-  AttendParams p = p0;
+hipError_t launch_rows(const AttendParams& p, hipStream_t s) {
   // no sequence is longer than its line of the page table
   const int64_t cap = (p.ld_pages * p.c.page_tokens + kStep - 1) / kStep, steps = cap > 0 ? cap : 1;
   const int64_t units = (int64_t)p.sequences * p.c.heads * p.row_tiles, most = units * steps;
   const unsigned runs = (unsigned)(most < p.max_runs ? most : p.max_runs);
-  p.min_steps = 1;
   const bool full = p.c.dim == DT;
   if (p.rht && full) ufp4_attend_kernel<GRID, DT, R, 2, true><<<runs, kAtThreads, 0, s>>>(p);
   else if (p.rht) ufp4_attend_kernel<GRID, DT, R, 2, false><<<runs, kAtThreads, 0, s>>>(p);
@@ -800,7 +801,7 @@ hipError_t launch_rows(const AttendParams& p0, hipStream_t s) {
   else ufp4_attend_kernel<GRID, DT, R, 1, false><<<runs, kAtThreads, 0, s>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || steps == 1) return e;
-  ufp4_attend_join_kernel<GRID, R><<<dim3(runs, (unsigned)(R * (p.c.dim / 32))), kAtThreads, 0, s>>>(p);
+  ufp4_attend_join_kernel<GRID, R><<<runs * (unsigned)(R * (p.c.dim / 32)), kAtThreads, 0, s>>>(p);
   return hipGetLastError();
 }
 

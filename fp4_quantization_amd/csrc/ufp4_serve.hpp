@@ -9,7 +9,6 @@
 namespace ufp4 {
 
 // ------------------------------------------------------------------ products
-constexpr int kMvTokens = 64;  // tokens a workgroup multiplies at once
 constexpr int kMvChunk = 128;  // values of K a step
 
 struct MatvecParams {
@@ -93,7 +92,6 @@ struct AttendParams {
   float scale;
   int32_t row_tiles;  // of a sequence with max_draft drafted tokens
   int32_t max_runs;   // of a launch
-  int32_t min_steps;  // of a run
   SplitUnit* split;   // [run]
   float2* ml;         // [run][2][row]: maximum and sum
   float* o;           // [run][2][row][dim]
