@@ -11,6 +11,10 @@
 //     two for each token.
 //   MX32: bf16, which has the range of the power-of-two scales; x' is the sum of
 //     one or three bf16 numbers.
+//
+// Bound by reading the weights.  One token, kernel times: 65536 x 8192 (302 MB) 63 to
+// 65 us, 4.7 TB/s, where reading alone takes 48; 4096 x 4096 7.5, reading alone 5.9
+// with its launch.  16 tokens, 16384 x 4096: 11.9, and 4 for x'.
 #include "ufp4_expand.hpp"
 #include "ufp4_serve.hpp"
 #include "ufp4_vec.hpp"

@@ -502,7 +502,7 @@ int ufp4_gemm_grouped_dw(const ufp4_config* cfg, int64_t M, int64_t N, int64_t p
  *   MX32: as a sum of bf16 numbers: one, exact, for bf16 x without the
  *     transform, else three (24 bits).  Weights and products below 2^-126 may
  *     count as zero.
- * Meant for few tokens: the weights are read once for every 64 of them.
+ * Meant for few tokens: the weights are read once for every 16 to 64 of them.
  * cfg: grid, scaling, rht, rht_seed.  K % 32 == 0, K and N below 2^25, tokens
  * below 2^21 (UFP4_ERR_SHAPE); codes 16-byte and NV16 scales 2-byte aligned.  tokens or N
  * of 0 writes nothing, K of 0 writes zeros.
