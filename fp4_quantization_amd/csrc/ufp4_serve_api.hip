@@ -182,8 +182,12 @@ size_t ufp4_tree_attention_workspace(const ufp4_cache* cache, int32_t q_heads, i
   if (cache_shape(cache) || q_heads < 1 || q_heads > 8192 || q_heads % cache->heads || sequences < 0 ||
       sequences > kMaxSequences || max_draft < 1 || max_draft >= kMaxRows / q_heads)
     return 0;
-  const int group = q_heads / cache->heads, rows = attend_rows(cache->dim, group, max_draft);
-  return attend_ws(attend_runs(cache->dim, rows), rows, cache->dim);
+  // fewer drafted tokens may take tiles of fewer rows and more runs: enough for them too
+  const int group = q_heads / cache->heads, least = attend_rows(cache->dim, group, 1);
+  const int rows = attend_rows(cache->dim, group, max_draft);
+  const size_t few = attend_ws(attend_runs(cache->dim, least), least, cache->dim);
+  const size_t all = attend_ws(attend_runs(cache->dim, rows), rows, cache->dim);
+  return few > all ? few : all;
 }
 
 int ufp4_tree_attention(const ufp4_config* cfg, const ufp4_cache* cache, const uint16_t* q, int64_t ldq,

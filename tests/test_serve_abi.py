@@ -179,3 +179,16 @@ def test_attention_tensors(F):
                       ("bf16", dict(q=torch.zeros(5, 1024)))):
         with pytest.raises(TypeError, match=match):
             call(**kw)
+
+
+def test_workspaces_of_larger_calls_do_for_smaller_ones(F):
+    """A workspace for up to so many tokens is large enough for fewer of them."""
+    for dim in (32, 64, 96, 128, 192, 256):
+        for heads in (2, 8, 16, 64):
+            c = cache(F, dim=dim)
+            sizes = [F.lib.ufp4_tree_attention_workspace(ctypes.byref(c), heads, 3, n) for n in range(1, 65)]
+            assert sizes[0] > 0 and sizes == sorted(sizes)
+    for K in (32, 4096, 65536):
+        for scaling in (0, 1):
+            sizes = [F.lib.ufp4_matvec_workspace(cfg_of(F, scaling=scaling), n, 64, K) for n in range(1, 130)]
+            assert sizes == sorted(sizes)
