@@ -26,10 +26,7 @@ namespace {
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kMvWaves = 8, kMvThreads = 64 * kMvWaves;
-constexpr int kSegment = 4;  // chunks of a wave whose weights are on the way at once
-constexpr int kLdsTokens = 4;
-constexpr size_t kLdsX = 96 << 10;  // bytes
+constexpr int kMvThreads = 64 * kMvWaves;
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ float pow2f(int e) { return __uint_as_float((uint32_t)(e + 127) << 23); }  // normal e
@@ -298,11 +295,6 @@ __device__ __forceinline__ void store_y(const MatvecParams& p, int64_t at, const
   }
 }
 
-// Where the fragments of x' come from: LDS, where every workgroup has prepared them
-// (up to four tokens); registers, read once from what the kernel above prepared
-// (one fragment a step, K of one segment); or that memory, tile by tile.
-enum XSource { kXLds, kXRegisters, kXMemory };
-
 // Rows of w in tiles of 16, walked over by the workgroups.  kw of the eight waves
 // share a tile's chunks of K, and their sums meet in LDS; 8 / kw tiles side by side.
 // A wave's weights are loaded a segment (four chunks) ahead of their use, the first
@@ -412,7 +404,7 @@ __global__ __launch_bounds__(kMvThreads, X == kXRegisters ? 2 : 4) void ufp4_mat
   }
   auto piece = [&](int n, int c, int i, int q) { return xf[n][(((size_t)c * 4 + i) * PARTS + q) * 4 * TP]; };
   v32x4 xr[X == kXRegisters ? kSegment : 1][4];
-  if (X == kXRegisters) {
+  if (X == kXRegisters && chunks > 0) {  // (without chunks there is no x' to read)
 #pragma unroll
     for (int j = 0; j < kSegment; ++j)
 #pragma unroll
@@ -496,50 +488,29 @@ __global__ __launch_bounds__(kMvThreads, X == kXRegisters ? 2 : 4) void ufp4_mat
   }
 }
 
-constexpr int kCus = 256;
-
-// Waves that share a tile: those that have a whole segment of K each, and more where
-// that leaves waves of the device (16 a compute unit) without work.  One token, N x K
-// = 65536 x 8192: 70 us with 1, 2, 4 or 8; 4096 x 4096: 19, 12.5, 9.5, 7.5; 16 tokens,
-// 16384 x 4096: 26.6, 15.7, 16.2, 14.3.
-int log_waves(int64_t tiles, int64_t chunks) {
-  int log_kw = 0;
-  while (log_kw < 3 && (kSegment << log_kw) < chunks) ++log_kw;
-  while (log_kw < 3 && (2 << log_kw) <= chunks && (tiles << log_kw) < 16 * kCus) ++log_kw;
-  return log_kw;
-}
-
 template <int GRID, bool MX, int PARTS, bool APART>
 hipError_t launch_apart(const MatvecParams& p, hipStream_t s) {
-  const int64_t tiles = (p.N + 15) / 16, chunks = (p.K + kMvChunk - 1) / kMvChunk;
-  const int log_kw = log_waves(tiles, chunks), side = kMvWaves >> log_kw;
-  const int64_t groups = (tiles + side - 1) / side;
-  const unsigned gx = (unsigned)(groups < 2 * kCus ? groups : 2 * kCus);
-  if (matvec_in_lds(p.tokens, p.K, PARTS)) {
-    const size_t lds = (size_t)chunks * kMvChunk * p.tokens * PARTS * 2;
-    ufp4_matvec_kernel<GRID, MX, PARTS, 1, kXLds, APART><<<gx, kMvThreads, lds, s>>>(p, log_kw);
+  const MatvecPlan m = matvec_plan(p.tokens, p.N, p.K, PARTS);
+  const dim3 grid((unsigned)m.gx, (unsigned)m.gy);
+  if (m.x == kXLds) {
+    const size_t lds = (size_t)((p.K + kMvChunk - 1) / kMvChunk) * kMvChunk * p.tokens * PARTS * 2;
+    ufp4_matvec_kernel<GRID, MX, PARTS, 1, kXLds, APART><<<grid, kMvThreads, lds, s>>>(p, m.log_kw);
     return hipGetLastError();
   }
-  const int64_t t16 = (p.tokens + 15) / 16;
   if (p.K > 0) {
-    const int64_t parts = (p.K + 16 * kPrepareThreads - 1) / (16 * kPrepareThreads);
+    const int64_t parts = (p.K + 16 * kPrepareThreads - 1) / (16 * kPrepareThreads), t16 = (p.tokens + 15) / 16;
     ufp4_matvec_prepare_kernel<MX, PARTS><<<dim3((unsigned)(16 * t16), (unsigned)(parts < 8 ? parts : 8)), kPrepareThreads, 0, s>>>(p);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  // as many tokens a workgroup as leave every compute unit one
-  int nt = t16 > 2 ? 4 : (int)t16;
-  while (nt > 1 && groups * ((t16 + nt - 1) / nt) < kCus) nt /= 2;
-  const dim3 grid(gx, (unsigned)((t16 + nt - 1) / nt));
-  if (nt == 1 && PARTS == 1 && chunks <= (kSegment << log_kw)) {
-    const dim3 one(gx < kCus ? gx : kCus, grid.y);
-    if constexpr (PARTS == 1) ufp4_matvec_kernel<GRID, MX, PARTS, 1, kXRegisters, APART><<<one, kMvThreads, 0, s>>>(p, log_kw);
-  } else if (nt == 1) {
-    ufp4_matvec_kernel<GRID, MX, PARTS, 1, kXMemory, APART><<<grid, kMvThreads, 0, s>>>(p, log_kw);
-  } else if (nt == 2) {
-    ufp4_matvec_kernel<GRID, MX, PARTS, 2, kXMemory, APART><<<grid, kMvThreads, 0, s>>>(p, log_kw);
+  if (m.x == kXRegisters) {
+    if constexpr (PARTS == 1) ufp4_matvec_kernel<GRID, MX, PARTS, 1, kXRegisters, APART><<<grid, kMvThreads, 0, s>>>(p, m.log_kw);
+  } else if (m.nt == 1) {
+    ufp4_matvec_kernel<GRID, MX, PARTS, 1, kXMemory, APART><<<grid, kMvThreads, 0, s>>>(p, m.log_kw);
+  } else if (m.nt == 2) {
+    ufp4_matvec_kernel<GRID, MX, PARTS, 2, kXMemory, APART><<<grid, kMvThreads, 0, s>>>(p, m.log_kw);
   } else {
-    ufp4_matvec_kernel<GRID, MX, PARTS, 4, kXMemory, APART><<<grid, kMvThreads, 0, s>>>(p, log_kw);
+    ufp4_matvec_kernel<GRID, MX, PARTS, 4, kXMemory, APART><<<grid, kMvThreads, 0, s>>>(p, m.log_kw);
   }
   return hipGetLastError();
 }
@@ -562,11 +533,7 @@ hipError_t launch_parts(const MatvecParams& p, hipStream_t s) {
 
 }  // namespace
 
-bool matvec_in_lds(int64_t tokens, int64_t K, int parts) {
-  if (tokens > kLdsTokens) return false;
-  const int64_t padded = (K + kMvChunk - 1) / kMvChunk * kMvChunk;
-  return padded * tokens * parts * 2 <= (int64_t)kLdsX;
-}
+bool matvec_in_lds(int64_t tokens, int64_t K, int parts) { return matvec_fits_lds(tokens, K, parts); }
 
 hipError_t launch_matvec(const MatvecParams& p, hipStream_t s) {
   const int parts = matvec_parts(p.mx, p.rht, p.x_f32, p.y_f32);

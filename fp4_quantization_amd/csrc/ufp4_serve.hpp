@@ -4,13 +4,12 @@
 // is ufp4.h).
 #pragma once
 #include "ufp4_internal.hpp"
+#include "ufp4_matvec_plan.hpp"
 #include "ufp4_moe.hpp"
 
 namespace ufp4 {
 
 // ------------------------------------------------------------------ products
-constexpr int kMvChunk = 128;  // values of K a step
-
 struct MatvecParams {
   const void* x;
   int32_t x_f32, y_f32;
