@@ -42,6 +42,12 @@ constexpr int kAtWaves = 4, kAtThreads = 64 * kAtWaves;
 constexpr int attend_waves(int dt, int r) { return dt > 128 ? (r > 1 ? 1 : 2) : (r > 1 ? 2 : 3); }
 constexpr int kStep = 32 * kAtWaves;  // tokens
 constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147181f;
+// Softmax weights enter the second product as fp16, in units that bring the largest, 1,
+// to 2^15: fp16's 11 bits hold down to 2^-29 of it, and a weight is lost below 2^-40.
+// (As they are, at most 1, the cut is at 2^-25: of 131072 tokens that one other exceeds
+// by 18 in their logits, those of its wave were lost, a quarter of them.)  The factor is
+// exact, and no time is measured for it.
+constexpr float kWeightUnit = 32768.0f;
 
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 __device__ __forceinline__ double pow2d(int e) { return __longlong_as_double((long long)(e + 1023) << 52); }
@@ -616,7 +622,7 @@ __global__ __launch_bounds__(kAtThreads, attend_waves(DT, R)) void ufp4_attend_k
         for (int j = 0; j < 8; ++j) {
           const float e = __builtin_amdgcn_exp2f(y[j] - base);
           l += e;
-          pf[i][j] = (_Float16)e;
+          pf[i][j] = (_Float16)(e * kWeightUnit);
         }
         sum[i] = sum[i] * alpha + l;
         if (__any(alpha != 1.0f)) {
@@ -673,7 +679,7 @@ __global__ __launch_bounds__(kAtThreads, attend_waves(DT, R)) void ufp4_attend_k
       const float base = m == -__builtin_inff() ? 0.0f : m;
 #pragma unroll
       for (int k = 0; k < kAtWaves; ++k) l += ml[k][1][16 * i + r] * __builtin_amdgcn_exp2f(ml[k][0][16 * i + r] - base);
-      const float alpha = __builtin_amdgcn_exp2f(mx[i] - base);
+      const float alpha = __builtin_amdgcn_exp2f(mx[i] - base) * (1.0f / kWeightUnit);
       mx[i] = m;
       sum[i] = l;
       // values 32 t + 8 g + 2 k + parity, from row 4 g + k of the two tiles

@@ -588,7 +588,8 @@ int ufp4_cache_read(const ufp4_config* cfg, const ufp4_cache* cache, const int64
  *   page_table: int32 [sequences][ld_pages]; the tokens of a page that is
  *     outside [0, pages) are seen by no row.
  * Logits are exact products in fp32 sums (transformed q in 22 bits), the softmax
- * fp32; its weights enter the second product as fp16.
+ * fp32; its weights enter the second product as fp16, rounded to 11 bits down to
+ * 2^-29 of the largest so far, to multiples of 2^-39 of it below.
  * cfg: NV16 only; grid, rht, rht_seed.  softmax_scale finite.  1 <= q_heads <=
  * 8192, 1 <= max_draft, sequences <= 65535, q_rows < 2^28,
  * ld_pages * page_tokens <= 2^30 (UFP4_ERR_INVALID_ARGUMENT,
