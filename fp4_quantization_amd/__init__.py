@@ -607,9 +607,10 @@ class _Scratch:
     calls, but calls that may run at the same time need one each."""
 
     def __init__(self, nbytes: int, device):
-        self.nbytes = int(nbytes)
-        self.buf = torch.empty(self.nbytes, dtype=torch.uint8, device=device)
-        self.ptr = self.buf.data_ptr()
+        self.buf = torch.empty(int(nbytes), dtype=torch.uint8, device=device)
+
+    ptr = property(lambda self: self.buf.data_ptr())
+    nbytes = property(lambda self: self.buf.nbytes)
 
 
 class MatvecWorkspace(_Scratch):
@@ -653,6 +654,14 @@ class QCache:
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
                  k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):
+        self._tensors = (k_codes, k_scales, v_codes, v_scales, k_scale, v_scale)
+        self._present = tuple(t for t in self._tensors if t is not None)
+        self._lay_out()
+        self.pages, self.page_tokens, self.heads, self.dim = self._c.pages, self._c.page_tokens, self._c.heads, self._c.dim
+
+    def _lay_out(self) -> None:
+        """Checks the buffers, and takes their addresses."""
+        k_codes, k_scales, v_codes, v_scales, k_scale, v_scale = self._tensors
         if k_codes.dim() != 4:
             raise ValueError("k_codes must be [pages, heads, page_tokens, dim / 2]")
         pages, heads, tokens, half = k_codes.shape
@@ -666,13 +675,13 @@ class QCache:
         for t in (k_scale, v_scale):
             if t is not None and (t.dtype != torch.float32 or tuple(t.shape) != (heads,) or not t.is_contiguous()):
                 raise ValueError("tensor scales must be contiguous float32 [heads]")
-        self.pages, self.heads, self.page_tokens, self.dim = pages, heads, tokens, 2 * half
-        # the buffers stay those of this object: their addresses are laid out once
-        self._tensors = (k_codes, k_scales, v_codes, v_scales, k_scale, v_scale)
-        self._c = ufp4_cache(*(_ptr(t) for t in self._tensors), pages, tokens, heads, 2 * half)
         device = k_codes.get_device()
-        if any(t is not None and t.get_device() != device for t in self._tensors):
+        if any(t.get_device() != device for t in self._present):
             raise ValueError("all buffers of the cache must lie on one device")
+        c = ufp4_cache(*(_ptr(t) for t in self._tensors), pages, tokens, heads, 2 * half)
+        if hasattr(self, "_c") and (pages, tokens, heads, 2 * half) != (self.pages, self.page_tokens, self.heads, self.dim):
+            raise ValueError("the buffers of a cache must keep its geometry")
+        self._c, self._memory = c, [(t.data_ptr(), t.nbytes) for t in self._present]
 
     k_codes = property(lambda self: self._tensors[0])
     k_scales = property(lambda self: self._tensors[1])
@@ -682,6 +691,10 @@ class QCache:
     v_scale = property(lambda self: self._tensors[5])
 
     def c(self) -> ufp4_cache:
+        # a buffer can get other memory (.data, resize_): compared at every call (0.8 us),
+        # checked in full (2 us) only after it did
+        if [(t.data_ptr(), t.nbytes) for t in self._present] != self._memory:
+            self._lay_out()
         return self._c
 
 
