@@ -650,7 +650,9 @@ class QCache:
     """Device buffers of a 4-bit key-value cache (the layouts of ufp4_cache):
     k_codes uint8 [pages, heads, page_tokens, dim / 2], k_scales [.., dim / 16],
     v_codes uint8 [pages, heads, page_tokens / 32, dim / 2, 32], v_scales [..,
-    dim / 16, 32]; k_scale and v_scale float32 [heads] tensor scales, None: 1."""
+    dim / 16, 32]; k_scale and v_scale float32 [heads] tensor scales, None: 1.
+    A buffer may get other memory of the same shape (.data); one that no longer
+    fits is refused by the next call."""
 
     def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor, v_scales: torch.Tensor,
                  k_scale: torch.Tensor | None = None, v_scale: torch.Tensor | None = None):

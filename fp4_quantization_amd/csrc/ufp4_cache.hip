@@ -277,8 +277,11 @@ hipError_t launch_read(const CacheParams& p0, hipStream_t s) {
   CacheParams p = p0;
   p.pieces = fast_div((uint32_t)p.c.dim / (p.out_f32 ? 4 : 16));
   const int64_t bytes = p.tokens * p.c.heads * p.c.dim * (p.out_f32 ? 4 : 2) * ((p.k_out != nullptr) + (p.v_out != nullptr));
-  // past the caches where most of it would not stay in them: 256 MB of results 60 us,
-  // through them 92
+  // past the caches where results and what else lies there do not fit.  Keys and values of
+  // 8 x 128, bf16, outputs of three calls in turn, past the caches / through them: 128 MiB
+  // 38 / 38 us, 160 45 / 47, 192 54 / 67, 256 69 / 108; with a kernel behind that reads
+  // both 69 / 67, 98 / 101, 119 / 122, 174 / 172.  fp32, 4 x 160: 96 MiB 23 / 28, 160 37 /
+  // 44, 256 59 / 99, read again 51 / 50, 92 / 101, 176 / 176.
   const bool past = bytes > kLastLevelCache / 2;
   if (p.out_f32 && past) ufp4_cache_read_kernel<GRID, float, true><<<grid_of(p), kCacheThreads, 0, s>>>(p);
   else if (p.out_f32) ufp4_cache_read_kernel<GRID, float, false><<<grid_of(p), kCacheThreads, 0, s>>>(p);

@@ -24,7 +24,11 @@ struct MatvecParams {
   uint16_t* xp;
   int32_t* shift;
 };
-// 16-bit numbers that x' is split into.
+// 16-bit numbers that x' is split into, one where that is exact.  For a bf16 result one
+// fp16 number does as well: off by 2^-11 where the result's own rounding is off by 2^-8
+// (errors of whole results, that rounding included, are 0.7 to 0.9% larger than from
+// fp32 x'), for half the MFMAs and LDS of two.  fp32 results take two (22 bits); MX32,
+// whose numbers are bf16, three (24).
 inline int matvec_parts(bool mx, bool rht, bool x_f32, bool y_f32) {
   if (mx) return rht || x_f32 ? 3 : 1;
   return y_f32 && (rht || x_f32) ? 2 : 1;

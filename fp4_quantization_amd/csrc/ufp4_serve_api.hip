@@ -9,7 +9,7 @@ using namespace ufp4;
 namespace {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 25;
-constexpr int64_t kMaxTokens = (int64_t)1 << 21;  // of a product: a launch has 2^16 blocks of 64 in y
+constexpr int64_t kMaxTokens = (int64_t)1 << 21;  // of a product: at most 2^15 blocks of 64 in y (smaller ones only below 256 workgroups)
 constexpr int64_t kMaxLd = 0x7FFFFFFF;  // of a cache call's rows
 constexpr int64_t kMaxRows = (int64_t)1 << 28;
 constexpr int32_t kMaxSequences = 65535;  // of a launch in y

@@ -500,8 +500,8 @@ int ufp4_gemm_grouped_dw(const ufp4_config* cfg, int64_t M, int64_t N, int64_t p
  *     bf16 y, two (22 bits) for fp32 y.  A bf16 x without the transform is exact
  *     in one down to 2^-28 of the token's largest.
  *   MX32: as a sum of bf16 numbers: one, exact, for bf16 x without the
- *     transform, else three (24 bits).  Weights and products below 2^-126 may
- *     count as zero.
+ *     transform, else three (24 bits, of x' below 2^-110 multiples of 2^-133).
+ *     Weights and products below 2^-126 may count as zero.
  * Meant for few tokens: the weights are read once for every 16 to 64 of them.
  * cfg: grid, scaling, rht, rht_seed.  K % 32 == 0, K and N below 2^25, tokens
  * below 2^21 (UFP4_ERR_SHAPE); codes 16-byte and NV16 scales 2-byte aligned.  tokens or N
@@ -576,6 +576,9 @@ int ufp4_cache_read(const ufp4_config* cfg, const ufp4_cache* cache, const int64
  *     <q[row][h], k_j> over them, k and v of head h / (q_heads / heads);
  *   lse[row][h] = ln of the sum of exp(softmax_scale <q, k_j>) (may be NULL).
  * A row that sees nothing gets zeros, lse -infinity.
+ * Meant for few rows: a sequence's keys and values are read and expanded once for
+ * every 16 (or, where there are more, 32) rows of drafted tokens times query heads
+ * of a key head, so a prompt's chain costs its whole history for every 32 of them.
  * q [q_rows][ldq] and out [q_rows][ldo], bf16, head h at columns h * dim; any
  * 2-byte alignment; lse fp32 [q_rows][q_heads], dense; q_heads a multiple of
  * heads.  With cfg->rht the cache holds transformed keys and values: q is
